@@ -110,6 +110,10 @@ typedef int32_t qg_status;
 #define QG_QGEMM_MAX_K  133120  /* k of the W8A8 prefill GEMM: the largest multiple
                                    of 128 with k * 127^2 < 2^31, so that the int32
                                    sums are exact for any codes                      */
+#define QG_MAX_ROW_GROUPS 1024  /* groups (experts, adapters) of a row plan           */
+#define QG_MAX_PLAN_ROWS (1 << 30)  /* rows of a row plan                             */
+#define QG_MAX_TOP_K    16      /* experts per token of qg_moe_route                  */
+#define QG_LORA_MAX_R   256     /* rank of a low-rank adapter                         */
 
 /* Human-readable text for a status code (static storage). */
 const char* qg_status_str(qg_status s);
@@ -711,6 +715,151 @@ qg_status qg_qgemm_w8a8(const int8_t* xq, const float* s_x, const void* x_out, i
                         int64_t m, int64_t k, int32_t n_out,
                         const int8_t* wq, const float* s_w, const void* w_out, int32_t w_out_ld,
                         int64_t n, float* y, int32_t* acc_out, void* stream);
+
+/*
+ * Products whose matrix depends on the row: a row plan (which rows go with
+ * which matrix), a top-k router that makes one, int8 products grouped by
+ * expert, and low-rank adapters of many requests.  They stand beside the
+ * products above, which use one matrix for all rows; the pages describe none
+ * of them, so the definitions here are this library's.
+ *
+ * Row plan.  ids[rows] holds a group number per row; the plan is
+ *   order[rows]         : the rows whose id is in [0, groups), sorted by id
+ *                         (stable: equal ids keep their order), then -1;
+ *   offsets[groups + 1] : group g's rows are order[offsets[g] ..
+ *                         offsets[g + 1] - 1];
+ *   pos[rows]           : where a row stands in order, -1 if its id is
+ *                         outside [0, groups) (a row without a matrix).
+ * All int32 on the device.  A plan serves any number of calls.  The kernels
+ * that read one stay in bounds whatever it holds (offsets are clamped into
+ * [0, rows] and made ascending, source rows into x); a plan that is not one
+ * gives unspecified numbers.
+ *
+ * qg_group_rows: ids, order, pos: [rows]; offsets: [groups + 1]; 1 <= rows <=
+ *   QG_MAX_PLAN_ROWS, 1 <= groups <= QG_MAX_ROW_GROUPS.  ws:
+ *   qg_group_rows_workspace_bytes(rows, groups) bytes, 16-B aligned (may be
+ *   NULL when that is 0); its contents on entry do not matter.
+ */
+size_t qg_group_rows_workspace_bytes(int64_t rows, int32_t groups);  /* 0 if out of range, too */
+qg_status qg_group_rows(const int32_t* ids, int64_t rows, int32_t groups, int32_t* offsets, int32_t* order,
+                        int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Top-k router and the plan of its choice.  For each token t with logits
+ * l[e], e < experts:
+ *   slot j < top_k holds the expert with the j-th largest logit (equal
+ *   logits: the lowest expert first);
+ *   w[j] = exp(l[j] - max l) / sum of exp(l - max l), the sum over the chosen
+ *   experts (renorm != 0) or over all experts (renorm == 0).
+ * A logit of -inf (a masked expert) or NaN is never chosen and adds nothing;
+ * +inf counts as the largest finite fp32.  Slots that find no expert hold id
+ * -1 and weight 0 (all of a token's, if all its logits are masked).
+ * logits : [tokens][experts] of type xt (QG_F32 or QG_BF16), aligned to its
+ *          elements.
+ * ids    : [tokens][top_k] int32 (out); weights: [tokens][top_k] fp32 (out).
+ * offsets, order, pos: the plan of ids as rows = tokens * top_k pairs, pair
+ *          p = t * top_k + j (out).
+ * 1 <= top_k <= min(experts, QG_MAX_TOP_K); experts <= QG_MAX_ROW_GROUPS;
+ * tokens * top_k <= QG_MAX_PLAN_ROWS.  ws as qg_group_rows of
+ * (tokens * top_k, experts).
+ */
+qg_status qg_moe_route(const void* logits, int32_t xt, int64_t tokens, int32_t experts, int32_t top_k,
+                       int32_t renorm, int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* pos,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* A plan as the products take it (host struct, device pointers). */
+typedef struct qg_row_groups {
+    const int32_t* offsets;  /* [groups + 1]                                          */
+    const int32_t* order;    /* [rows], or NULL: x is in the plan's order already      */
+    int64_t rows;
+    int32_t groups;
+    int32_t per_row;         /* rows of the plan per row of x (top_k): row p of the    */
+                             /* plan reads row p / per_row of x                       */
+} qg_row_groups;
+
+/*
+ * The experts' int8 matrices, one after the other (host struct, device
+ * pointers): codes as QG_WFMT_INT8 [e][n][k], or each expert's codes in 16-row
+ * tiles as QG_WFMT_INT8_T16 ([e][qg_tiles16_bytes(n, k)] bytes); scale
+ * [e][n] (the multiplier s_w, as qg_quantize_absmax gives it).
+ */
+typedef struct qg_experts {
+    int32_t fmt;
+    int32_t reserved;
+    int64_t e, n, k;
+    const int8_t* codes;
+    const float* scale;
+} qg_experts;
+
+/*
+ * Products grouped by expert.  Sorted row i of expert g reads row src of x,
+ * src = order[i] / per_row (i itself where order is NULL):
+ *   amode QG_ACT_FLOAT (W8A16): y[i][n] = (sum_k codes[g][n][k] x[src][k]) / s_w[g][n],
+ *     x bf16 [x_rows][k], the products exact, fp32 sums;
+ *   amode QG_ACT_INT8 (W8A8): y[i][n] = acc / (s_w[g][n] s_x[src]), acc =
+ *     sum_k codes[g][n][k] x[src][k] (int32, exact), x int8 codes [x_rows][k]
+ *     with a scale s_x per row, as qg_quantize_absmax (QG_PER_ROW) gives them.
+ * Group sizes are ragged and known to the device only; a group may be empty.
+ * Rows of y at and past offsets[groups] are left as they were.
+ *
+ * qg_qgemm_experts        : y [rows][n] of type yt (QG_F32 or QG_BF16).
+ * qg_qgemm_experts_swiglu : y[i][n] = a / (1 + exp(-a)) * b, a and b the
+ *   products with the gate and the up matrix (same e, n, k and fmt), in fp32.
+ * qg_qgemm_experts_combine: y [tokens][n], y[t] = sum over the slots j <
+ *   per_row, in order, of weights[t][j] * (product row pos[t * per_row + j]);
+ *   pos outside [0, rows) adds nothing.  pos, weights: [tokens][per_row];
+ *   rows = tokens * per_row.  The products are held in fp32 in ws
+ *   (qg_experts_combine_workspace_bytes(rows, n) bytes, 16-B aligned).
+ * Results of one call are deterministic; which kernel runs depends on the
+ * sizes alone, and kernels differ in summation order.
+ *
+ * k % 128 == 0, 128 <= k <= QG_BATCH_MAX_K (QG_QGEMM_MAX_K for QG_ACT_INT8);
+ * 1 <= n < 2^30; e = groups <= QG_MAX_ROW_GROUPS; e * n * k, x_rows * k and
+ * rows * n <= 2^40; 1 <= x_rows < 2^31, and x_rows >= rows where order is
+ * NULL; per_row in [1, QG_MAX_TOP_K].  codes, x and y 16-B aligned; the other
+ * arrays aligned to their elements.  Outputs must not overlap inputs.
+ */
+qg_status qg_qgemm_experts(const qg_experts* w, const qg_row_groups* groups, int32_t amode, const void* x,
+                           const float* s_x, int64_t x_rows, void* y, int32_t yt, void* stream);
+qg_status qg_qgemm_experts_swiglu(const qg_experts* gate, const qg_experts* up, const qg_row_groups* groups,
+                                  int32_t amode, const void* x, const float* s_x, int64_t x_rows, void* y,
+                                  int32_t yt, void* stream);
+size_t qg_experts_combine_workspace_bytes(int64_t rows, int64_t n);  /* 0 if out of range */
+qg_status qg_qgemm_experts_combine(const qg_experts* w, const qg_row_groups* groups, int32_t amode, const void* x,
+                                   const float* s_x, int64_t x_rows, const int32_t* pos, const float* weights,
+                                   int64_t tokens, void* y, int32_t yt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests, added to the outputs of up to
+ * QG_MAX_GROUP projections that read the same x (q, k and v; gate and up):
+ *   y_m[t] += scale_m[g] B_m[g] (A_m[g] x[t]),  g the group of row t,
+ * for the rows t that the plan names (order not NULL, per_row == 1, its
+ * entries distinct); rows without an adapter are left as they were.  Products
+ * exact, sums in fp32, A x never rounded below fp32; y is rounded once (bf16
+ * to nearest even).  Results are deterministic.
+ * m : HOST array of count descriptors: a bf16 [groups][r][k], b bf16
+ *     [groups][n][r], scale fp32 [groups] or NULL (1), y [x_rows][n] of type yt.
+ * x : bf16 [x_rows][k].
+ * r % 8 == 0, 8 <= r <= QG_LORA_MAX_R (each matrix its own); k % 128 == 0,
+ * 128 <= k <= QG_BATCH_MAX_K; 1 <= n < 2^30; rows <= x_rows < 2^31;
+ * groups <= QG_MAX_ROW_GROUPS; x_rows * k, x_rows * n, groups * n * r and
+ * groups * r * k <= 2^40.  a, b, x, y 16-B aligned.
+ * ws: qg_lora_workspace_bytes(...) bytes for the same m (its r), count,
+ *     rows, groups and k, 16-B aligned; contents on entry do not matter.
+ *     Calls that overlap on one workspace race.
+ */
+typedef struct qg_lora {
+    const void* a;
+    const void* b;
+    const float* scale;
+    int64_t n;
+    int32_t r;
+    int32_t reserved;
+    void* y;
+} qg_lora;
+size_t qg_lora_workspace_bytes(const qg_lora* m, int32_t count, int64_t rows, int32_t groups, int64_t k);
+qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* groups, const void* x, int64_t x_rows,
+                      int64_t k, int32_t yt, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Measurement aid, not a step of the method: the streaming-read probe that

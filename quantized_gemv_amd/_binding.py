@@ -36,6 +36,10 @@ QG_BATCH_MAX_K = 262144
 QG_MX_BLOCK = 32
 QG_QGEMM_MAX_K = 133120
 QG_ABSMAX_SCRATCH_PARTS = 1024
+QG_MAX_ROW_GROUPS = 1024
+QG_MAX_PLAN_ROWS = 1 << 30
+QG_MAX_TOP_K = 16
+QG_LORA_MAX_R = 256
 QG_CHAIN_MAX_STAGES = 4096
 QG_CHAIN_MIN_K = 128
 QG_CHAIN_MAX_K = 16384
@@ -64,6 +68,20 @@ class CSepMatrix(ctypes.Structure):
 class CChainStage(ctypes.Structure):
     _fields_ = [("count", _c_i32), ("dep", _c_i32), ("x", _c_vp), ("w", ctypes.POINTER(CWeight)),
                 ("y", ctypes.POINTER(_c_vp))]
+
+
+class CRowGroups(ctypes.Structure):
+    _fields_ = [("offsets", _c_vp), ("order", _c_vp), ("rows", _c_i64), ("groups", _c_i32), ("per_row", _c_i32)]
+
+
+class CExperts(ctypes.Structure):
+    _fields_ = [("fmt", _c_i32), ("reserved", _c_i32), ("e", _c_i64), ("n", _c_i64), ("k", _c_i64),
+                ("codes", _c_vp), ("scale", _c_vp)]
+
+
+class CLora(ctypes.Structure):
+    _fields_ = [("a", _c_vp), ("b", _c_vp), ("scale", _c_vp), ("n", _c_i64), ("r", _c_i32), ("reserved", _c_i32),
+                ("y", _c_vp)]
 
 
 _SIGS = {
@@ -116,6 +134,21 @@ _SIGS = {
     "qg_qgemm_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i32]),
     "qg_qgemm_w8a8_outlier": (_c_i32, [_c_vp, _c_i64, _c_i64, _c_vp, _c_i32, _c_vp, _c_vp, _c_vp, _c_i32, _c_i64,
                                        _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "qg_group_rows_workspace_bytes": (_c_sz, [_c_i64, _c_i32]),
+    "qg_group_rows": (_c_i32, [_c_vp, _c_i64, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "qg_moe_route": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp,
+                              _c_sz, _c_vp]),
+    "qg_qgemm_experts": (_c_i32, [ctypes.POINTER(CExperts), ctypes.POINTER(CRowGroups), _c_i32, _c_vp, _c_vp, _c_i64,
+                                  _c_vp, _c_i32, _c_vp]),
+    "qg_qgemm_experts_swiglu": (_c_i32, [ctypes.POINTER(CExperts), ctypes.POINTER(CExperts),
+                                         ctypes.POINTER(CRowGroups), _c_i32, _c_vp, _c_vp, _c_i64, _c_vp, _c_i32,
+                                         _c_vp]),
+    "qg_experts_combine_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
+    "qg_qgemm_experts_combine": (_c_i32, [ctypes.POINTER(CExperts), ctypes.POINTER(CRowGroups), _c_i32, _c_vp, _c_vp,
+                                          _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i32, _c_vp, _c_sz, _c_vp]),
+    "qg_lora_workspace_bytes": (_c_sz, [ctypes.POINTER(CLora), _c_i32, _c_i64, _c_i32, _c_i64]),
+    "qg_lora_add": (_c_i32, [ctypes.POINTER(CLora), _c_i32, ctypes.POINTER(CRowGroups), _c_vp, _c_i64, _c_i64, _c_i32,
+                             _c_vp, _c_sz, _c_vp]),
     "qg_qgemm_w8a8": (_c_i32, [_c_vp, _c_vp, _c_vp, _c_i32, _c_i64, _c_i64, _c_i32, _c_vp, _c_vp, _c_vp, _c_i32,
                                _c_i64, _c_vp, _c_vp, _c_vp]),
 }
@@ -677,6 +710,330 @@ def qgemm_w8a8(xq: torch.Tensor, s_x: torch.Tensor, x_out: Optional[torch.Tensor
                                _p(w_out) if n_out else None, w_ld, n, _p(y), _p(acc_out), _stream(xq)),
            "qg_qgemm_w8a8")
     return y
+
+
+# ------------------------------------------------------------------ products whose matrix depends on the row
+
+def _same_device(x: torch.Tensor, *others: Optional[torch.Tensor]):
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError("tensors are on %s and %s" % (x.device, t.device))
+
+
+def _call(name: str, x: torch.Tensor, *args):
+    """The entry point `name` on x's current stream (appended as the last
+    argument), with x's device current for the launch."""
+    if x.device.index == torch.cuda.current_device():
+        _check(getattr(lib(), name)(*args, _stream(x)), name)
+    else:
+        with torch.cuda.device(x.device):
+            _check(getattr(lib(), name)(*args, _stream(x)), name)
+
+
+def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor):
+    """t, checked, or a new tensor of that shape and dtype on like's device."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    _same_device(like, t)
+    return t
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """(tensor or None, bytes) of a workspace of at least `need` bytes."""
+    if ws is None:
+        return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
+    _dev(ws, "ws", torch.uint8)
+    _same_device(like, ws)
+    return ws, ws.numel()
+
+
+@dataclass
+class RowGroups:
+    """A row plan (qg_group_rows): the rows sorted by group. offsets
+    [groups + 1], order and pos [rows], int32 on the device; per_row plan rows
+    read one row of x (a router's top_k)."""
+    offsets: torch.Tensor
+    order: torch.Tensor
+    pos: torch.Tensor
+    per_row: int = 1
+
+    def __post_init__(self):
+        for t, nm in ((self.offsets, "offsets"), (self.order, "order"), (self.pos, "pos")):
+            _dev(t, nm, torch.int32)
+        _same_device(self.offsets, self.order, self.pos)
+        if self.order.numel() != self.pos.numel():
+            raise ValueError("order and pos differ in length")
+
+    @property
+    def groups(self) -> int:
+        return self.offsets.numel() - 1
+
+    @property
+    def rows(self) -> int:
+        return self.order.numel()
+
+    def c_struct(self, gather: bool = True) -> CRowGroups:
+        return CRowGroups(self.offsets.data_ptr(), self.order.data_ptr() if gather else None, self.rows, self.groups,
+                          self.per_row)
+
+
+@dataclass
+class Routing:
+    """What moe_route returns: ids and weights [tokens][top_k] and the plan."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    groups: RowGroups
+
+
+def _plan_buffers(x: torch.Tensor, rows: int, groups: int, per_row: int, out: Optional[RowGroups]) -> RowGroups:
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=x.device)
+        return RowGroups(torch.empty(groups + 1, **i32), torch.empty(rows, **i32), torch.empty(rows, **i32), per_row)
+    if out.rows != rows or out.groups != groups or out.per_row != per_row:
+        raise ValueError("out holds %d rows of %d groups, per_row %d; %d, %d, %d needed"
+                         % (out.rows, out.groups, out.per_row, rows, groups, per_row))
+    _same_device(x, out.offsets)
+    return out
+
+
+def group_rows(ids: torch.Tensor, groups: int, out: Optional[RowGroups] = None,
+               ws: Optional[torch.Tensor] = None) -> RowGroups:
+    """Rows sorted by id (qg_group_rows): ids int32 [rows] (ids outside
+    [0, groups) have no group) -> RowGroups.  A serving step makes one plan of
+    its rows' adapters and uses it for every layer and projection."""
+    _dev(ids, "ids", torch.int32)
+    if ids.dim() != 1:
+        raise ValueError("ids must be [rows]")
+    rows = ids.numel()
+    out = _plan_buffers(ids, rows, groups, 1, out)
+    ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(rows, groups)), ids)
+    _call("qg_group_rows", ids, _p(ids), rows, groups, _p(out.offsets), _p(out.order), _p(out.pos), _p(ws), nws)
+    return out
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, out: Optional[Routing] = None,
+              ws: Optional[torch.Tensor] = None) -> Routing:
+    """Top-k router and the plan of its choice (qg_moe_route): logits
+    [tokens][experts] fp32 or bf16 -> Routing."""
+    _dev(logits, "logits", (torch.float32, torch.bfloat16))
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens][experts]")
+    t, e = logits.shape
+    ids = _shaped(None if out is None else out.ids, "out.ids", (t, top_k), torch.int32, logits)
+    weights = _shaped(None if out is None else out.weights, "out.weights", (t, top_k), torch.float32, logits)
+    plan = _plan_buffers(logits, t * top_k, e, top_k, None if out is None else out.groups)
+    ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(t * top_k, e)), logits)
+    _call("qg_moe_route", logits, _p(logits), _xt(logits), t, e, top_k, 1 if renorm else 0, _p(ids), _p(weights),
+          _p(plan.offsets), _p(plan.order), _p(plan.pos), _p(ws), nws)
+    return Routing(ids, weights, plan) if out is None else out
+
+
+@dataclass
+class QExperts:
+    """The experts' int8 matrices (qg_experts): codes [e][n][k] (QG_WFMT_INT8)
+    or each expert's 16-row tiles (QG_WFMT_INT8_T16, tiled16_experts), scale
+    [e][n]."""
+    fmt: int
+    e: int
+    n: int
+    k: int
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    def __post_init__(self):
+        _dev(self.codes, "codes", torch.int8)
+        _dev(self.scale, "scale", torch.float32)
+        _same_device(self.codes, self.scale)
+        per = (self.n + 15) // 16 * 16 if self.fmt == QG_WFMT_INT8_T16 else self.n
+        if self.codes.numel() != self.e * per * self.k or self.scale.numel() != self.e * self.n:
+            raise ValueError("codes or scale do not hold %d experts of [%d][%d]" % (self.e, self.n, self.k))
+        self._c = CExperts(self.fmt, 0, self.e, self.n, self.k, self.codes.data_ptr(), self.scale.data_ptr())
+
+    def c_struct(self) -> CExperts:
+        return self._c
+
+
+def quantize_experts(w: torch.Tensor) -> QExperts:
+    """Per-row absmax int8 (qg_quantize_absmax) of the experts' matrices
+    w [e][n][k] (fp32 or bf16)."""
+    if w.dim() != 3:
+        raise ValueError("w must be [e][n][k]")
+    e, n, k = w.shape
+    q, s = quantize_absmax(w.view(e * n, k), per_row=True)
+    return QExperts(QG_WFMT_INT8, e, n, k, q.view(e, n, k), s.view(e, n))
+
+
+def tiled16_experts(w: QExperts) -> QExperts:
+    """The QG_WFMT_INT8 experts w with each one's codes in 16-row tiles (one
+    qg_pack_tiles16 per expert; done once, when the weights are loaded)."""
+    if w.fmt != QG_WFMT_INT8:
+        raise ValueError("tiled16_experts takes QG_WFMT_INT8 experts")
+    nb = int(lib().qg_tiles16_bytes(w.n, w.k))
+    if nb == 0:
+        raise ValueError("shape (%d, %d) has no 16-row tiled layout" % (w.n, w.k))
+    out = torch.empty((w.e, nb), dtype=torch.int8, device=w.codes.device)
+    codes = w.codes.view(w.e, w.n, w.k)
+    for j in range(w.e):
+        pack_tiles16(codes[j], out[j])
+    return QExperts(QG_WFMT_INT8_T16, w.e, w.n, w.k, out, w.scale)
+
+
+def _experts_x(w: QExperts, x: torch.Tensor, groups: RowGroups, s_x: Optional[torch.Tensor], gather: bool) -> int:
+    """Checks x (bf16, or int8 codes with s_x) against w and the plan; the
+    activation mode."""
+    _dev(x, "x", (torch.bfloat16, torch.int8))
+    if x.dim() != 2 or x.shape[1] != w.k:
+        raise ValueError("x must be [rows][%d]" % w.k)
+    if (x.dtype == torch.int8) != (s_x is not None):
+        raise ValueError("int8 x needs s_x, bf16 x takes none")
+    if s_x is not None:
+        _dev(s_x, "s_x", torch.float32)
+        if s_x.numel() != x.shape[0]:
+            raise ValueError("s_x must hold one scale per row of x")
+    want = -(-groups.rows // groups.per_row) if gather else groups.rows
+    if x.shape[0] != want:
+        raise ValueError("x has %d rows, the plan reads %d" % (x.shape[0], want))
+    if groups.groups != w.e:
+        raise ValueError("the plan has %d groups for %d experts" % (groups.groups, w.e))
+    _same_device(x, w.codes, s_x, groups.offsets)
+    return QG_ACT_FLOAT if s_x is None else QG_ACT_INT8
+
+
+def _y_dtype(y: Optional[torch.Tensor], y_dtype):
+    dt = y_dtype if y is None else y.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("y is float32 or bfloat16")
+    return dt
+
+
+def qgemm_experts(w: QExperts, x: torch.Tensor, groups: RowGroups, s_x: Optional[torch.Tensor] = None,
+                  gather: bool = True, y_dtype=torch.float32, y: torch.Tensor = None) -> torch.Tensor:
+    """Products grouped by expert (qg_qgemm_experts): x bf16 [x_rows][k]
+    (W8A16), or int8 codes with s_x [x_rows] (W8A8). Returns y [rows][n] in the
+    plan's order; rows behind the last group are not written. gather=False: x
+    is in the plan's order already."""
+    amode = _experts_x(w, x, groups, s_x, gather)
+    y = _shaped(y, "y", (groups.rows, w.n), _y_dtype(y, y_dtype), x)
+    cg = groups.c_struct(gather)
+    _call("qg_qgemm_experts", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _p(x), _p(s_x), x.shape[0], _p(y),
+          _xt(y))
+    return y
+
+
+def qgemm_experts_swiglu(gate: QExperts, up: QExperts, x: torch.Tensor, groups: RowGroups,
+                         s_x: Optional[torch.Tensor] = None, gather: bool = True, y_dtype=torch.bfloat16,
+                         y: torch.Tensor = None) -> torch.Tensor:
+    """silu(gate product) * up product, grouped by expert, in one launch
+    (qg_qgemm_experts_swiglu). Returns y [rows][n] in the plan's order."""
+    amode = _experts_x(gate, x, groups, s_x, gather)
+    _same_device(x, up.codes)
+    y = _shaped(y, "y", (groups.rows, gate.n), _y_dtype(y, y_dtype), x)
+    cg = groups.c_struct(gather)
+    _call("qg_qgemm_experts_swiglu", x, ctypes.byref(gate.c_struct()), ctypes.byref(up.c_struct()), ctypes.byref(cg),
+          amode, _p(x), _p(s_x), x.shape[0], _p(y), _xt(y))
+    return y
+
+
+def qgemm_experts_combine(w: QExperts, x: torch.Tensor, groups: RowGroups, weights: torch.Tensor,
+                          s_x: Optional[torch.Tensor] = None, gather: bool = False, y_dtype=torch.float32,
+                          y: torch.Tensor = None, ws: torch.Tensor = None) -> torch.Tensor:
+    """Products grouped by expert, added per token with the router's weights
+    [tokens][top_k] (qg_qgemm_experts_combine). x is in the plan's order (the
+    output of qgemm_experts_swiglu) unless gather. Returns y [tokens][n]."""
+    amode = _experts_x(w, x, groups, s_x, gather)
+    _dev(weights, "weights", torch.float32)
+    tokens = groups.rows // groups.per_row
+    if weights.numel() != groups.rows or tokens * groups.per_row != groups.rows:
+        raise ValueError("weights must be [tokens][%d], one per row of the plan" % groups.per_row)
+    _same_device(x, weights)
+    y = _shaped(y, "y", (tokens, w.n), _y_dtype(y, y_dtype), x)
+    ws, nws = _workspace(ws, int(lib().qg_experts_combine_workspace_bytes(groups.rows, w.n)), x)
+    cg = groups.c_struct(gather)
+    _call("qg_qgemm_experts_combine", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _p(x), _p(s_x), x.shape[0],
+          _p(groups.pos), _p(weights), tokens, _p(y), _xt(y), _p(ws), nws)
+    return y
+
+
+def moe_ffn(x: torch.Tensor, logits: torch.Tensor, gate: QExperts, up: QExperts, down: QExperts, top_k: int,
+            renorm: bool = True, act_int8: bool = False, y_dtype=torch.bfloat16) -> torch.Tensor:
+    """The expert feed-forward of x bf16 [tokens][k]: moe_route of the
+    router's logits, SwiGLU of the gate and up products, the down product
+    combined per token. act_int8: both products W8A8, their activations
+    quantized per row (quantize_absmax). Returns y [tokens][down.n]."""
+    r = moe_route(logits, top_k, renorm)
+    s_x = s_h = None
+    if act_int8:
+        x, s_x = quantize_absmax(x, per_row=True)
+    h = qgemm_experts_swiglu(gate, up, x, r.groups, s_x=s_x)
+    if act_int8:
+        h, s_h = quantize_absmax(h, per_row=True)
+    return qgemm_experts_combine(down, h, r.groups, r.weights, s_x=s_h, y_dtype=y_dtype)
+
+
+@dataclass
+class LoraAdapters:
+    """Low-rank adapters of one projection: a [groups][r][k] and b
+    [groups][n][r] bf16, scale fp32 [groups] or None (1)."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        _dev(self.a, "a", torch.bfloat16)
+        _dev(self.b, "b", torch.bfloat16)
+        if self.a.dim() != 3 or self.b.dim() != 3 or self.a.shape[0] != self.b.shape[0] or self.a.shape[1] != self.b.shape[2]:
+            raise ValueError("a must be [groups][r][k] and b [groups][n][r]")
+        if self.scale is not None:
+            _dev(self.scale, "scale", torch.float32)
+            if self.scale.numel() != self.a.shape[0]:
+                raise ValueError("scale must be [groups]")
+        _same_device(self.a, self.b, self.scale)
+
+
+class LoraLaunch:
+    """Pre-marshalled arguments of one qg_lora_add call: the adapters of
+    1..QG_MAX_GROUP projections of the same x, added to ys (kept alive by this
+    object, with a workspace); launch() enqueues it on x's current stream."""
+
+    def __init__(self, x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters],
+                 ys: Sequence[torch.Tensor], ws: Optional[torch.Tensor] = None):
+        _dev(x, "x", torch.bfloat16)
+        n = len(adapters)
+        if not 1 <= n <= QG_MAX_GROUP or len(ys) != n:
+            raise ValueError("need 1..%d adapters and as many outputs" % QG_MAX_GROUP)
+        if x.dim() != 2 or x.shape[0] != groups.rows:
+            raise ValueError("x must be [%d][k], a row per row of the plan" % groups.rows)
+        _same_device(x, groups.offsets)
+        m, k = x.shape
+        for ad, y in zip(adapters, ys):
+            _dev(y, "y", (torch.float32, torch.bfloat16))
+            _same_device(x, ad.a, y)
+            if ad.a.shape[0] != groups.groups or ad.a.shape[2] != k:
+                raise ValueError("a must be [%d][r][%d]" % (groups.groups, k))
+            if tuple(y.shape) != (m, ad.b.shape[1]) or y.dtype != ys[0].dtype:
+                raise ValueError("each y must be [%d][n] of its b, all of one dtype" % m)
+        self.m = (CLora * n)(*[
+            CLora(ad.a.data_ptr(), ad.b.data_ptr(), None if ad.scale is None else ad.scale.data_ptr(), ad.b.shape[1],
+                  ad.a.shape[1], 0, y.data_ptr()) for ad, y in zip(adapters, ys)])
+        self.ws, self.nws = _workspace(ws, int(lib().qg_lora_workspace_bytes(self.m, n, m, groups.groups, k)), x)
+        self.cg = groups.c_struct()
+        self.x, self.keep = x, (groups, list(adapters), list(ys))
+        self.args = (self.m, n, ctypes.byref(self.cg), _p(x), m, k, _xt(ys[0]), _p(self.ws), self.nws)
+
+    def launch(self):
+        _call("qg_lora_add", self.x, *self.args)
+
+
+def lora_add(x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters], ys: Sequence[torch.Tensor],
+             ws: Optional[torch.Tensor] = None):
+    """Adds the rows' low-rank adapters (qg_lora_add) to the projections' outputs
+    ys [rows][n], in place: x bf16 [rows][k], groups = group_rows of the rows'
+    adapter numbers (rows without one are left as they were). Returns ys."""
+    LoraLaunch(x, groups, adapters, ys, ws).launch()
+    return ys
 
 
 def chain_plan_image(stages, workgroups: int):

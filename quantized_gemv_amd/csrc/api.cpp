@@ -80,6 +80,72 @@ qg_status check_out_operand(const void* p, int32_t ld, int32_t n_out) {
     return QG_OK;
 }
 
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+constexpr int64_t kMaxElems = (int64_t)1 << 40;
+inline bool fits(int64_t a, int64_t b) { return a <= kMaxElems / b; }  // a * b <= 2^40, b >= 1
+
+// A row plan as the products read it.
+qg_status check_groups(const qg_row_groups* g) {
+    if (!g->offsets) return QG_ERR_NULLPTR;
+    if (g->rows < 1 || g->rows > QG_MAX_PLAN_ROWS) return QG_ERR_SHAPE;
+    if (g->groups < 1 || g->groups > QG_MAX_ROW_GROUPS) return QG_ERR_SHAPE;
+    if (g->per_row < 1 || g->per_row > QG_MAX_TOP_K) return QG_ERR_SHAPE;
+    if (!aligned_to(g->offsets, 4) || !aligned_to(g->order, 4)) return QG_ERR_ALIGN;
+    return QG_OK;
+}
+
+// The checks the expert products share; fills everything but the second
+// matrix.
+qg_status check_experts(const qg_experts* w, const qg_row_groups* g, int32_t amode, const void* x, const float* s_x,
+                        int64_t x_rows, const void* y, int32_t yt, qg::ExpertArgs* a) {
+    if (!w || !g || !x || !y || !w->codes || !w->scale) return QG_ERR_NULLPTR;
+    if (amode != QG_ACT_FLOAT && amode != QG_ACT_INT8) return QG_ERR_ARG;
+    if (amode == QG_ACT_INT8 && !s_x) return QG_ERR_NULLPTR;
+    if (yt != QG_F32 && yt != QG_BF16) return QG_ERR_ARG;
+    if (w->fmt != QG_WFMT_INT8 && w->fmt != QG_WFMT_INT8_T16) return QG_ERR_ARG;
+    const qg_status st = check_groups(g);
+    if (st != QG_OK) return st;
+    if (w->e != g->groups || w->n < 1 || w->n >= ((int64_t)1 << 30)) return QG_ERR_SHAPE;
+    if (w->k < 128 || w->k % 128 != 0 || w->k > (amode == QG_ACT_INT8 ? QG_QGEMM_MAX_K : QG_BATCH_MAX_K))
+        return QG_ERR_SHAPE;
+    if (!fits(w->e * w->n, w->k) || x_rows < 1 || x_rows >= ((int64_t)1 << 31) || !fits(x_rows, w->k) ||
+        !fits(g->rows, w->n))
+        return QG_ERR_SHAPE;
+    if (!g->order && x_rows < g->rows) return QG_ERR_SHAPE;
+    if (!aligned16(w->codes) || !aligned16(x) || !aligned16(y)) return QG_ERR_ALIGN;
+    if (!aligned_to(w->scale, 4) || !aligned_to(s_x, 4)) return QG_ERR_ALIGN;
+    a->e = w->e;
+    a->n = w->n;
+    a->k = w->k;
+    a->codes = w->codes;
+    a->scale = w->scale;
+    a->codes2 = nullptr;
+    a->scale2 = nullptr;
+    a->t16 = w->fmt == QG_WFMT_INT8_T16;
+    a->act_int8 = amode == QG_ACT_INT8;
+    a->x = x;
+    a->s_x = s_x;
+    a->x_rows = x_rows;
+    a->offsets = g->offsets;
+    a->order = g->order;
+    a->per_row = g->per_row;
+    a->rows = g->rows;
+    a->y = const_cast<void*>(y);
+    a->yt = yt;
+    return QG_OK;
+}
+
+// Sum of the ranks rounded up to 16; 0 if a rank or the count is out of range.
+int64_t lora_padded_rank(const qg_lora* m, int32_t count) {
+    if (!m || count < 1 || count > QG_MAX_GROUP) return 0;
+    int64_t sum = 0;
+    for (int32_t j = 0; j < count; ++j) {
+        if (m[j].r < 8 || m[j].r > QG_LORA_MAX_R || m[j].r % 8 != 0) return 0;
+        sum += (m[j].r + 15) / 16 * 16;
+    }
+    return sum;
+}
+
 // Sizes the prefill GEMM supports: K in whole 128-column steps and small
 // enough that the int32 sums are exact (K * 127^2 < 2^31), indices of the
 // [m][k] / [n][k] operands within 2^40 elements, m and n below 2^31.
@@ -654,6 +720,150 @@ qg_status qg_qgemm_w8a8_outlier(const void* x, int64_t m, int64_t k, const int32
     e = qg::launch_qgemm(a, as_stream(stream));
     if (e != hipSuccess || !dbg) return from_hip(e);
     return debug_result(as_stream(stream));
+}
+
+size_t qg_group_rows_workspace_bytes(int64_t rows, int32_t groups) {
+    if (rows < 1 || rows > QG_MAX_PLAN_ROWS || groups < 1 || groups > QG_MAX_ROW_GROUPS) return 0;
+    return qg::group_workspace(rows, groups);
+}
+
+qg_status qg_group_rows(const int32_t* ids, int64_t rows, int32_t groups, int32_t* offsets, int32_t* order,
+                        int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
+    static_assert(QG_MAX_ROW_GROUPS == qg::kMaxRowGroups, "header and library agree");
+    if (!ids || !offsets || !order || !pos) return QG_ERR_NULLPTR;
+    if (rows < 1 || rows > QG_MAX_PLAN_ROWS || groups < 1 || groups > QG_MAX_ROW_GROUPS) return QG_ERR_SHAPE;
+    if (!aligned_to(ids, 4) || !aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(pos, 4))
+        return QG_ERR_ALIGN;
+    const size_t need = qg_group_rows_workspace_bytes(rows, groups);
+    if (need && (!ws || ws_bytes < need)) return QG_ERR_WORKSPACE;
+    if (need && !aligned16(ws)) return QG_ERR_ALIGN;
+    const qg::GroupArgs a = {ids, rows, groups, offsets, order, pos, ws};
+    return from_hip(qg::launch_group_rows(a, as_stream(stream)));
+}
+
+qg_status qg_moe_route(const void* logits, int32_t xt, int64_t tokens, int32_t experts, int32_t top_k,
+                       int32_t renorm, int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* pos,
+                       void* ws, size_t ws_bytes, void* stream) {
+    if (!logits || !ids || !weights || !offsets || !order || !pos) return QG_ERR_NULLPTR;
+    if (xt != QG_F32 && xt != QG_BF16) return QG_ERR_ARG;
+    if (experts < 1 || experts > QG_MAX_ROW_GROUPS || top_k < 1 || top_k > QG_MAX_TOP_K || top_k > experts)
+        return QG_ERR_SHAPE;
+    if (tokens < 1 || tokens > QG_MAX_PLAN_ROWS / top_k) return QG_ERR_SHAPE;
+    if (!aligned_to(logits, xt == QG_F32 ? 4 : 2) || !aligned_to(ids, 4) || !aligned_to(weights, 4) ||
+        !aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(pos, 4))
+        return QG_ERR_ALIGN;
+    const int64_t rows = tokens * top_k;
+    const size_t need = qg_group_rows_workspace_bytes(rows, experts);
+    if (need && (!ws || ws_bytes < need)) return QG_ERR_WORKSPACE;
+    if (need && !aligned16(ws)) return QG_ERR_ALIGN;
+    qg::RouteArgs a;
+    a.logits = logits;
+    a.xt = xt;
+    a.tokens = tokens;
+    a.top_k = top_k;
+    a.renorm = renorm != 0;
+    a.weights = weights;
+    a.ids = ids;
+    a.group = {ids, rows, experts, offsets, order, pos, ws};
+    return from_hip(qg::launch_moe_route(a, as_stream(stream)));
+}
+
+qg_status qg_qgemm_experts(const qg_experts* w, const qg_row_groups* groups, int32_t amode, const void* x,
+                           const float* s_x, int64_t x_rows, void* y, int32_t yt, void* stream) {
+    qg::ExpertArgs a;
+    const qg_status st = check_experts(w, groups, amode, x, s_x, x_rows, y, yt, &a);
+    if (st != QG_OK) return st;
+    return from_hip(qg::launch_experts(a, as_stream(stream)));
+}
+
+qg_status qg_qgemm_experts_swiglu(const qg_experts* gate, const qg_experts* up, const qg_row_groups* groups,
+                                  int32_t amode, const void* x, const float* s_x, int64_t x_rows, void* y,
+                                  int32_t yt, void* stream) {
+    qg::ExpertArgs a;
+    if (!up) return QG_ERR_NULLPTR;
+    qg_status st = check_experts(up, groups, amode, x, s_x, x_rows, y, yt, &a);
+    if (st != QG_OK) return st;
+    a.codes2 = up->codes;
+    a.scale2 = up->scale;
+    if (!gate || !gate->codes || !gate->scale) return QG_ERR_NULLPTR;
+    if (gate->fmt != up->fmt) return QG_ERR_ARG;
+    if (gate->e != up->e || gate->n != up->n || gate->k != up->k) return QG_ERR_SHAPE;
+    if (!aligned16(gate->codes) || !aligned_to(gate->scale, 4)) return QG_ERR_ALIGN;
+    a.codes = gate->codes;
+    a.scale = gate->scale;
+    return from_hip(qg::launch_experts(a, as_stream(stream)));
+}
+
+size_t qg_experts_combine_workspace_bytes(int64_t rows, int64_t n) {
+    if (rows < 1 || rows > QG_MAX_PLAN_ROWS || n < 1 || n >= ((int64_t)1 << 30) || !fits(rows, n)) return 0;
+    return (size_t)rows * (size_t)n * sizeof(float);
+}
+
+qg_status qg_qgemm_experts_combine(const qg_experts* w, const qg_row_groups* groups, int32_t amode, const void* x,
+                                   const float* s_x, int64_t x_rows, const int32_t* pos, const float* weights,
+                                   int64_t tokens, void* y, int32_t yt, void* ws, size_t ws_bytes, void* stream) {
+    qg::ExpertArgs a;
+    if (!pos || !weights) return QG_ERR_NULLPTR;
+    const qg_status st = check_experts(w, groups, amode, x, s_x, x_rows, y, yt, &a);
+    if (st != QG_OK) return st;
+    if (tokens < 1 || tokens > QG_MAX_PLAN_ROWS || tokens * groups->per_row != groups->rows) return QG_ERR_SHAPE;
+    if (!aligned_to(pos, 4) || !aligned_to(weights, 4)) return QG_ERR_ALIGN;
+    if (!ws || ws_bytes < qg_experts_combine_workspace_bytes(groups->rows, w->n)) return QG_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QG_ERR_ALIGN;
+    a.y = ws;
+    a.yt = QG_F32;
+    const hipError_t e = qg::launch_experts(a, as_stream(stream));
+    if (e != hipSuccess) return QG_ERR_HIP;
+    const qg::CombineArgs c = {static_cast<const float*>(ws), groups->rows, w->n, pos, weights, tokens,
+                               groups->per_row, y, yt};
+    return from_hip(qg::launch_combine(c, as_stream(stream)));
+}
+
+size_t qg_lora_workspace_bytes(const qg_lora* m, int32_t count, int64_t rows, int32_t groups, int64_t k) {
+    const int64_t rank = lora_padded_rank(m, count);
+    if (rank == 0 || rows < 1 || rows > QG_MAX_PLAN_ROWS || groups < 1 || groups > QG_MAX_ROW_GROUPS || k < 128 ||
+        k % 128 != 0 || k > QG_BATCH_MAX_K)
+        return 0;
+    return qg::lora_workspace(rows, groups, k, rank);
+}
+
+qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* groups, const void* x, int64_t x_rows,
+                      int64_t k, int32_t yt, void* ws, size_t ws_bytes, void* stream) {
+    if (!m || !groups || !x) return QG_ERR_NULLPTR;
+    if (count < 1 || count > QG_MAX_GROUP) return QG_ERR_ARG;
+    if (yt != QG_F32 && yt != QG_BF16) return QG_ERR_ARG;
+    if (!groups->order) return QG_ERR_NULLPTR;
+    const qg_status st = check_groups(groups);
+    if (st != QG_OK) return st;
+    if (groups->per_row != 1) return QG_ERR_SHAPE;
+    if (k < 128 || k % 128 != 0 || k > QG_BATCH_MAX_K) return QG_ERR_SHAPE;
+    if (x_rows < groups->rows || x_rows >= ((int64_t)1 << 31) || !fits(x_rows, k)) return QG_ERR_SHAPE;
+    if (!aligned16(x)) return QG_ERR_ALIGN;
+    qg::LoraArgs a;
+    for (int32_t j = 0; j < count; ++j) {
+        const qg_lora& mj = m[j];
+        if (!mj.a || !mj.b || !mj.y) return QG_ERR_NULLPTR;
+        if (mj.r < 8 || mj.r > QG_LORA_MAX_R || mj.r % 8 != 0) return QG_ERR_SHAPE;
+        if (mj.n < 1 || mj.n >= ((int64_t)1 << 30) || !fits(x_rows, mj.n) || !fits(mj.n * groups->groups, mj.r) ||
+            !fits((int64_t)mj.r * groups->groups, k))
+            return QG_ERR_SHAPE;
+        if (!aligned16(mj.a) || !aligned16(mj.b) || !aligned16(mj.y) || !aligned_to(mj.scale, 4)) return QG_ERR_ALIGN;
+        a.m[j] = {static_cast<const uint16_t*>(mj.a), static_cast<const uint16_t*>(mj.b), mj.scale, mj.n, mj.r, mj.y};
+    }
+    const size_t need = qg_lora_workspace_bytes(m, count, groups->rows, groups->groups, k);
+    if (!ws || need == 0 || ws_bytes < need) return QG_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QG_ERR_ALIGN;
+    a.count = count;
+    a.yt = yt;
+    a.x = static_cast<const uint16_t*>(x);
+    a.x_rows = x_rows;
+    a.k = k;
+    a.offsets = groups->offsets;
+    a.order = groups->order;
+    a.groups = groups->groups;
+    a.rows = groups->rows;
+    a.ws = ws;
+    return from_hip(qg::launch_lora(a, as_stream(stream)));
 }
 
 size_t qg_probe_stream_read_bytes(int64_t bytes, int32_t workgroups) {

@@ -132,6 +132,90 @@ hipError_t launch_quantize_mxfp4(const void* x, int xt, int64_t rows, int64_t co
 hipError_t launch_gemm_mxfp4(const uint8_t* a, const uint8_t* as, int64_t m, int64_t k, const uint8_t* b,
                              const uint8_t* bs, int64_t n, float* y, hipStream_t st);
 
+// Rows sorted by a group number: offsets [groups + 1], order [rows], pos
+// [rows]; ws of group_workspace() bytes (0 for a single chunk).
+constexpr int kMaxRowGroups = 1024;
+struct GroupArgs {
+    const int32_t* ids;
+    int64_t rows;
+    int32_t groups;
+    int32_t* offsets;
+    int32_t* order;
+    int32_t* pos;
+    void* ws;
+};
+size_t group_workspace(int64_t rows, int64_t groups);
+hipError_t launch_group_rows(const GroupArgs& a, hipStream_t st);
+// The router writes ids and weights, then groups the ids (group.ids = ids).
+struct RouteArgs {
+    const void* logits;
+    int xt;
+    int64_t tokens;
+    int top_k, renorm;
+    int32_t* ids;
+    float* weights;
+    GroupArgs group;
+};
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t st);
+
+// Expert products over sorted rows: y[i] = x[order[i] / per_row] W_e^T for
+// the rows i of expert e (order null: x row i).  codes2 / scale2: the up
+// matrices of a SwiGLU launch (null: one product per row).
+struct ExpertArgs {
+    int64_t e, n, k;
+    const int8_t* codes;
+    const float* scale;
+    const int8_t* codes2;
+    const float* scale2;
+    bool t16, act_int8;
+    const void* x;
+    const float* s_x;
+    int64_t x_rows;
+    const int32_t* offsets;
+    const int32_t* order;
+    int32_t per_row;
+    int64_t rows;
+    void* y;
+    int yt;
+};
+hipError_t launch_experts(const ExpertArgs& a, hipStream_t st);
+// out[t][n] = sum over j of weights[t][j] * h[pos[t][j]][n] (pos outside
+// [0, rows): nothing)
+struct CombineArgs {
+    const float* h;
+    int64_t rows, n;
+    const int32_t* pos;
+    const float* weights;
+    int64_t tokens;
+    int top_k;
+    void* y;
+    int yt;
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
+
+// Low-rank adapters of one x: y[m][t] += scale[g] B[g] (A[g] x[t]).
+struct LoraMat {
+    const uint16_t* a;   // [groups][r][k]
+    const uint16_t* b;   // [groups][n][r]
+    const float* scale;  // [groups] or null
+    int64_t n;
+    int32_t r;
+    void* y;             // [x_rows][n]
+};
+struct LoraArgs {
+    LoraMat m[kMaxGroupLaunch];
+    int count, yt;
+    const uint16_t* x;
+    int64_t x_rows, k;
+    const int32_t* offsets;
+    const int32_t* order;
+    int32_t groups;
+    int64_t rows;
+    void* ws;
+};
+size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int64_t padded_rank);
+hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
+
 int device_cu_count();
 
 // Streaming-read probe: workgroups of kQProbeThreads each read one block of

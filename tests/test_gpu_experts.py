@@ -1,0 +1,331 @@
+"""GPU expert products (qg_qgemm_experts, _swiglu, _combine) and the expert
+feed-forward against the fp64 oracle on the same codes, scales and inputs.
+
+Tolerances.  W8A16: exact products, fp32 sums of K terms; as for the other
+W8A16 products, 1e-5 of the row's largest output (TOL_F32).  W8A8: int32 sums
+are exact, so y carries the roundings of float(acc), the scales' product or
+reciprocals, and the quotient: at most 8 half steps of 2^-24, elementwise.
+SwiGLU: |silu'| <= 1.1, so its error is 1.1 |dg| |u| + |silu(g)| |du| plus 8
+half steps for exp, sum, quotient and product.  Combine: the products' errors
+times |w|, plus one rounding per slot.  bf16 outputs add half a step, 2^-8."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import TOL_F32, bf16_to_f64, dev, dev_bf16, host
+from oracle import rows as R
+import synth
+
+pytestmark = pytest.mark.gpu
+HALF = 2.0 ** -24
+
+
+def note(msg):
+    print("[case] " + msg, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def qg():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import quantized_gemv_amd as q
+    q.lib()
+    return q
+
+
+class Case:
+    """Codes, scales, activations and a plan on both sides."""
+
+    def __init__(self, qg, t, e, top, k, n, act8, tiled, seed, mats=1, spread="even", drop=0.0, gather=True):
+        g = synth.rng(seed)
+        self.t, self.e, self.top, self.k, self.n, self.act8, self.gather = t, e, top, k, n, act8, gather
+        if spread == "even":
+            ids = np.stack([g.permutation(e)[:top] for _ in range(t)])
+        elif spread == "one":            # every token's first slot the same expert
+            ids = np.stack([np.roll(np.arange(e), -(e // 2))[:top] for _ in range(t)])
+        else:                            # skewed: expert j with weight 1 / (1 + j)^2
+            p = 1.0 / (1 + np.arange(e)) ** 2
+            ids = np.stack([g.choice(e, size=top, replace=False, p=p / p.sum()) for _ in range(t)])
+        ids = np.where(g.random(ids.shape) < drop, -1, ids).astype(np.int32)
+        self.offsets, self.order, self.pos = R.group_rows(ids, e)
+        self.live = int(self.offsets[-1])
+        self.weights = g.random((t, top)).astype(np.float32)
+        rows = t if gather else t * top
+        if act8:
+            self.x = g.integers(-127, 128, (rows, k)).astype(np.int8)
+            self.s_x = (20 + 40 * g.random(rows)).astype(np.float32)
+            self.xd, self.sxd = dev(self.x), dev(self.s_x)
+        else:
+            bits = synth.to_bf16_bits(synth.gaussian(g, (rows, k), 1.0))
+            self.x, self.s_x = synth.bf16_bits_to_f32(bits), None
+            self.xd, self.sxd = dev_bf16(bits), None
+        self.codes = [g.integers(-127, 128, (e, n, k)).astype(np.int8) for _ in range(mats)]
+        # products of about unit size
+        unit = 73.0 * np.sqrt(k)
+        self.scale = [(unit * (0.5 + g.random((e, n)))).astype(np.float32) for _ in range(mats)]
+        self.w = []
+        for c, s in zip(self.codes, self.scale):
+            w = qg.QExperts(qg.QG_WFMT_INT8, e, n, k, dev(c), dev(s))
+            self.w.append(qg.tiled16_experts(w) if tiled else w)
+        self.groups = qg.RowGroups(dev(self.offsets), dev(self.order), dev(self.pos), top)
+
+    def products(self, j=0):
+        """(y, tolerance) of matrix j, live rows only."""
+        y = R.y_experts(self.codes[j], self.scale[j], self.x, self.offsets, self.order if self.gather else None,
+                        self.top, self.s_x)[:self.live]
+        if self.act8:
+            return y, 8 * HALF * np.abs(y)
+        return y, np.repeat(TOL_F32 * np.abs(y).max(axis=1, keepdims=True), self.n, axis=1) if self.live else y
+
+    def swiglu(self):
+        (g, dg), (u, du) = self.products(0), self.products(1)
+        y = R.y_swiglu(g, u)
+        silu = R.y_swiglu(g, np.ones_like(g))
+        return y, 1.1 * dg * np.abs(u) + np.abs(silu) * du + 8 * HALF * np.abs(y)
+
+    def combine(self):
+        y, dy = self.products()
+        out = R.y_combine(y, self.pos, self.weights)
+        tol = R.y_combine(dy, self.pos, self.weights) + self.top * HALF * R.y_combine(np.abs(y), self.pos, self.weights)
+        return out, tol
+
+
+def out_buffer(rows, n, bf16, guard=64):
+    full = torch.empty(rows * n + 2 * guard, dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    full.view(torch.uint8).fill_(0x5A)
+    return full, full[guard:guard + rows * n].view(rows, n)
+
+
+def check(full, y, live, want, tol, bf16, guard=64):
+    """Rows below `live` within tolerance; the rest and the guards untouched."""
+    raw = full.view(torch.uint8).cpu().numpy()
+    isz = full.dtype.itemsize
+    n = y.shape[1]
+    assert np.all(raw[:guard * isz] == 0x5A) and np.all(raw[(guard + live * n) * isz:] == 0x5A), "written outside"
+    got = host(y)[:live]
+    got = bf16_to_f64(got) if bf16 else got.astype(np.float64)
+    if bf16:
+        tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
+    bad = np.abs(got - want) - (tol + 1e-37)
+    assert np.all(bad <= 0), "off by up to %g at %s" % (bad.max(), np.unravel_index(np.argmax(bad), bad.shape))
+
+
+SIZES = [  # t, e, top, k, n, spread, drop
+    (1, 1, 1, 128, 1, "even", 0.0),
+    (1, 8, 2, 256, 40, "even", 0.0),
+    (2, 3, 1, 128, 16, "even", 0.5),
+    (5, 4, 4, 384, 33, "even", 0.2),
+    (16, 64, 8, 256, 96, "even", 0.0),
+    (15, 2, 1, 512, 130, "one", 0.0),
+    (16, 2, 1, 512, 128, "one", 0.0),
+    (17, 5, 2, 640, 129, "one", 0.0),
+    (33, 9, 3, 1024, 257, "skew", 0.1),
+    (64, 8, 2, 512, 200, "skew", 0.0),
+    (100, 16, 4, 384, 511, "skew", 0.1),
+    (130, 4, 2, 2176, 300, "even", 0.0),
+    (257, 3, 2, 256, 384, "one", 0.0),
+    (300, 70, 1, 128, 64, "skew", 0.0),
+    (600, 6, 2, 512, 520, "skew", 0.05),
+    (1100, 4, 1, 256, 272, "one", 0.0),
+]
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_experts(qg, size, act8, tiled):
+    t, e, top, k, n, spread, drop = size
+    bf16 = (t + n) % 2 == 1
+    note("experts %s act8=%s tiled=%s bf16=%s" % (size, act8, tiled, bf16))
+    c = Case(qg, t, e, top, k, n, act8, tiled, 31 * t + n, spread=spread, drop=drop)
+    full, y = out_buffer(t * top, n, bf16)
+    qg.qgemm_experts(c.w[0], c.xd, c.groups, s_x=c.sxd, y=y)
+    check(full, y, c.live, *c.products(), bf16)
+    # the same call again gives the same bits
+    z = torch.full_like(y, 7.0)
+    qg.qgemm_experts(c.w[0], c.xd, c.groups, s_x=c.sxd, y=z)
+    assert torch.equal(y[:c.live], z[:c.live]) and bool((z[c.live:] == 7.0).all())
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_swiglu(qg, size, act8, tiled):
+    t, e, top, k, n, spread, drop = size
+    bf16 = (t + n) % 2 == 0
+    note("swiglu %s act8=%s tiled=%s bf16=%s" % (size, act8, tiled, bf16))
+    c = Case(qg, t, e, top, k, n, act8, tiled, 37 * t + n, mats=2, spread=spread, drop=drop)
+    full, y = out_buffer(t * top, n, bf16)
+    qg.qgemm_experts_swiglu(c.w[0], c.w[1], c.xd, c.groups, s_x=c.sxd, y=y)
+    check(full, y, c.live, *c.swiglu(), bf16)
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_combine(qg, size, act8, gather):
+    t, e, top, k, n, spread, drop = size
+    bf16, tiled = (t + n) % 2 == 0, t % 2 == 0
+    note("combine %s act8=%s gather=%s tiled=%s bf16=%s" % (size, act8, gather, tiled, bf16))
+    c = Case(qg, t, e, top, k, n, act8, tiled, 41 * t + n, spread=spread, drop=drop, gather=gather)
+    full, y = out_buffer(t, n, bf16)
+    qg.qgemm_experts_combine(c.w[0], c.xd, c.groups, dev(c.weights), s_x=c.sxd, gather=gather, y=y)
+    check(full, y, t, *c.combine(), bf16)
+
+
+def test_all_rows_dropped(qg):
+    note("experts with every row dropped")
+    for act8 in (False, True):
+        c = Case(qg, 20, 4, 2, 256, 70, act8, True, 3, drop=1.1)
+        assert c.live == 0
+        full, y = out_buffer(40, 70, False)
+        qg.qgemm_experts(c.w[0], c.xd, c.groups, s_x=c.sxd, y=y)
+        torch.cuda.synchronize()
+        assert bool((full.view(torch.uint8) == 0x5A).all())
+        out = qg.qgemm_experts_combine(c.w[0], c.xd, c.groups, dev(c.weights), s_x=c.sxd, gather=True)
+        assert not host(out).any()
+
+
+def test_large_gates(qg):
+    note("swiglu with gates far from zero")
+    c = Case(qg, 40, 3, 1, 256, 64, False, True, 5, mats=2)
+    c.scale[0][:] = 1.0  # gates of several thousand, both signs
+    c.w[0].scale.copy_(dev(c.scale[0]))
+    full, y = out_buffer(40, 64, False)
+    qg.qgemm_experts_swiglu(c.w[0], c.w[1], c.xd, c.groups, y=y)
+    check(full, y, c.live, *c.swiglu(), False)
+
+
+def test_non_finite_rows_stay_alone(qg):
+    note("a row of infinities and NaN spoils no other row")
+    for t, e in ((16, 2), (600, 2)):
+        c = Case(qg, t, e, 1, 256, 96, False, True, 8, spread="one")
+        y0 = host(qg.qgemm_experts(c.w[0], c.xd, c.groups))
+        c.xd[3] = float("nan")
+        c.xd[7, 5] = float("inf")
+        y1 = host(qg.qgemm_experts(c.w[0], c.xd, c.groups))
+        rows = np.isin(c.order, [3, 7])
+        assert np.array_equal(y0[~rows], y1[~rows]) and not np.isfinite(y1[c.order == 3]).any()
+
+
+def test_long_k(qg):
+    note("experts with the largest k of each mode")
+    for k, act8 in ((qg.QG_BATCH_MAX_K, False), (qg.QG_QGEMM_MAX_K, True)):
+        for t in (3, 200):
+            c = Case(qg, t, 2, 1, k, 40, act8, t == 3, 9)
+            full, y = out_buffer(t, 40, False)
+            qg.qgemm_experts(c.w[0], c.xd, c.groups, s_x=c.sxd, y=y)
+            check(full, y, c.live, *c.products(), False)
+
+
+def test_weights_past_4_gib(qg):
+    note("experts whose codes and outputs pass 32-bit offsets")
+    # 5 experts of 1.07e9 codes: only the last ones are written, the rest stays zero
+    e, n, k = 5, 262144, 4096
+    codes = torch.zeros((e, n, k), dtype=torch.int8, device="cuda")
+    g = synth.rng(10)
+    rows = np.array([0, 1, n // 2, n - 1])
+    vals = g.integers(-127, 128, (len(rows), k)).astype(np.int8)
+    codes[e - 1, torch.from_numpy(rows).cuda()] = dev(vals)
+    scale = torch.full((e, n), 2000.0, device="cuda")
+    w = qg.QExperts(qg.QG_WFMT_INT8, e, n, k, codes, scale)
+    for t in (3, 200):
+        bits = synth.to_bf16_bits(synth.gaussian(g, (t, k), 1.0))
+        plan = qg.group_rows(torch.full((t,), e - 1, dtype=torch.int32, device="cuda"), e)
+        y = qg.qgemm_experts(w, dev_bf16(bits), plan)
+        got = y[:, torch.from_numpy(rows).cuda()]
+        want = synth.bf16_bits_to_f32(bits).astype(np.float64) @ vals.astype(np.float64).T / 2000.0
+        assert np.abs(host(got) - want).max() <= TOL_F32 * np.abs(want).max()
+        assert int((y != 0).sum()) <= t * len(rows)
+        del y, got
+
+
+def test_stream_and_graph(qg):
+    note("expert feed-forward on another stream, captured and replayed")
+    for t, act8 in ((4, False), (300, True)):
+        g = synth.rng(t)
+        e, top, k, f = 8, 2, 256, 384
+        gate, up, down = (qg.tiled16_experts(qg.quantize_experts(dev(synth.gaussian(g, s, 0.05))))
+                          for s in ((e, f, k), (e, f, k), (e, k, f)))
+        x = dev_bf16(synth.to_bf16_bits(synth.gaussian(g, (t, k), 1.0)))
+        logits = dev(synth.gaussian(g, (t, e), 1.0))
+
+        def step():
+            return qg.moe_ffn(x, logits, gate, up, down, top, act_int8=act8, y_dtype=torch.float32)
+
+        want = step().clone()
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            other = step()
+        st.synchronize()
+        assert torch.equal(other, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = step()
+        for seed in (1, 2, 3):
+            x.copy_(dev_bf16(synth.to_bf16_bits(synth.gaussian(synth.rng(seed), (t, k), 1.0))))
+            logits.copy_(dev(synth.gaussian(synth.rng(seed + 9), (t, e), 1.0)))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = y.clone()
+            assert torch.equal(got, step())
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("t", [1, 13, 200])
+def test_ffn(qg, t, act8):
+    """The whole feed-forward against the oracle's stages, each stage checked
+    on the tensors the stage before it gave (so its own tolerance applies)."""
+    note("moe_ffn t=%d act8=%s" % (t, act8))
+    g = synth.rng(50 + t)
+    e, top, k, f = 12, 3, 512, 640
+    ws = [qg.quantize_experts(dev(synth.gaussian(g, s, 0.05))) for s in ((e, f, k), (e, f, k), (e, k, f))]
+    bits = synth.to_bf16_bits(synth.gaussian(g, (t, k), 1.0))
+    l = synth.gaussian(g, (t, e), 1.0)
+    l[0, : e - 1] = -np.inf  # one expert left for the first token
+    y = host(qg.moe_ffn(dev_bf16(bits), dev(l), *ws, top, act_int8=act8, y_dtype=torch.float32))
+    r = qg.moe_route(dev(l), top)
+    ids, w = R.moe_route(l, top, True)
+    assert np.array_equal(host(r.ids), ids)
+    plan = R.group_rows(ids, e)
+    xd, s_x, s_h = dev_bf16(bits), None, None
+    if act8:
+        xd, s_x = qg.quantize_absmax(xd, per_row=True)
+    h = qg.qgemm_experts_swiglu(ws[0], ws[1], xd, r.groups, s_x=s_x)
+    hd = h
+    if act8:
+        hd, s_h = qg.quantize_absmax(h, per_row=True)
+    hh = host(hd).astype(np.float64) if act8 else bf16_to_f64(host(hd))
+    prod = R.y_experts(host(ws[2].codes), host(ws[2].scale), hh, plan[0], None, 1, None if s_h is None else host(s_h))
+    want = R.y_combine(prod, plan[2], host(r.weights))
+    assert np.abs(y - want).max() <= 2 * TOL_F32 * np.abs(prod[: plan[0][-1]]).max()
+
+
+def test_refusals(qg):
+    c = Case(qg, 8, 4, 2, 256, 32, False, False, 1, mats=2)
+    x, gr, w = c.xd, c.groups, c.w[0]
+    for bad in (x.float(), x[:, :128], x[:7], x.to(torch.int8), x.t()):
+        with pytest.raises(ValueError):
+            qg.qgemm_experts(w, bad, gr)
+    with pytest.raises(ValueError):
+        qg.qgemm_experts(w, x, gr, s_x=torch.ones(8, device="cuda"))
+    with pytest.raises(ValueError):
+        qg.qgemm_experts(w, x, gr, gather=False)
+    with pytest.raises(ValueError):
+        qg.qgemm_experts(w, x, gr, y_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        qg.qgemm_experts(w, x, gr, y=torch.empty((15, 32), device="cuda"))
+    with pytest.raises(ValueError):
+        qg.qgemm_experts(w, x, qg.group_rows(torch.zeros(8, dtype=torch.int32, device="cuda"), 3))
+    with pytest.raises(ValueError):
+        qg.QExperts(qg.QG_WFMT_INT8_T16, 4, 33, 256, w.codes, w.scale)
+    with pytest.raises(ValueError):
+        qg.qgemm_experts_combine(w, x, gr, torch.ones(15, device="cuda"), gather=True)
+    with pytest.raises(qg.QgError):
+        qg.qgemm_experts_swiglu(w, qg.tiled16_experts(c.w[1]), x, gr)
+    with pytest.raises(qg.QgError):
+        qg.qgemm_experts_combine(w, x, gr, dev(c.weights), gather=True,
+                                 ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
