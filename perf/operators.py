@@ -289,7 +289,7 @@ def run(state):
         import quantized_gemv_amd as qg
         if op == "route":
             r = s["kept"] = qg.moe_route(s["logits"], s["case"]["top"], renorm=s["case"]["renorm"], out=s.get("kept"))
-            return dict(ids=r.ids, weights=r.weights, order=r.groups.order, offsets=r.groups.offsets, pos=r.groups.pos)
+            return dict(ids=r.ids, weights=r.weights, order=r.groups.order, offsets=r.groups.offsets, pos=r.groups.pos.view(r.ids.shape))
         return _own_adapters(qg, s) if op == "adapters" else _own_experts(qg, s)
     if op == "route":
         return _plain_route(s)
