@@ -36,6 +36,12 @@ __device__ __forceinline__ void dma16(const void* src, void* lds_dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_ptr_t)lds_dst, 16, 0, 0);
 }
 
+// The same through a buffer resource: byte offset `voff` per lane, `soff`
+// uniform.
+__device__ __forceinline__ void dma16_buffer(__amdgpu_buffer_rsrc_t r, void* lds_dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds_dst, 16, voff, soff, 0, 0);
+}
+
 // s_waitcnt vmcnt(n) with expcnt / lgkmcnt left unconstrained (gfx9 encoding)
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {

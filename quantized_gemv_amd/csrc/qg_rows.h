@@ -28,9 +28,12 @@ __device__ __forceinline__ int wave_scan_incl(int v) {
     return v;
 }
 
-// One tile of up to MT sorted rows of one group.  rows == 0: no such tile.
+// One tile of up to MT sorted rows of one group (rows == 0: no such tile),
+// and the group it belongs to: its first row, its rows, and the tiles of the
+// groups before it.
 struct RowTile {
     int group, row0, rows;
+    int first, count, before;
 };
 
 // The tile-th tile of MT rows over all groups in ascending order, found by
@@ -40,7 +43,7 @@ struct RowTile {
 template <int MT>
 __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int tile) {
     const int lane = threadIdx.x & (kWave - 1);
-    RowTile t = {0, 0, 0};
+    RowTile t = {0, 0, 0, 0, 0, 0};
     int before = 0;
     for (int base = 0; base < groups; base += kWave) {
         const int g = base + lane;
@@ -57,7 +60,10 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
             t.group = base + l;
             const int first = __builtin_amdgcn_readlane(lo, l);
             const int last = __builtin_amdgcn_readlane(hi, l);
-            const int at = tile - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l));
+            t.before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l);
+            const int at = tile - t.before;
+            t.first = first;
+            t.count = last - first;
             t.row0 = first + at * MT;
             t.rows = min(MT, last - t.row0);
             break;
@@ -67,7 +73,25 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
     t.group = __builtin_amdgcn_readfirstlane(t.group);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    t.first = __builtin_amdgcn_readfirstlane(t.first);
+    t.count = __builtin_amdgcn_readfirstlane(t.count);
+    t.before = __builtin_amdgcn_readfirstlane(t.before);
     return t;
+}
+
+// Tiles of MT rows over all groups (uniform; all lanes active).
+template <int MT>
+__device__ __forceinline__ int count_row_tiles(const int32_t* __restrict__ offsets, int groups, int rows) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int sum = 0;
+    for (int base = 0; base < groups; base += kWave) {
+        const int g = base + lane;
+        if (g < groups) {
+            const int lo = min(max(offsets[g], 0), rows);
+            sum += (min(max(offsets[g + 1], lo), rows) - lo + MT - 1) / MT;
+        }
+    }
+    return wave_sum(sum);
 }
 
 // Most tiles of MT rows that `rows` rows in `groups` groups can make: every
