@@ -17,8 +17,7 @@ namespace qg {
 typedef __bf16 lbf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLWaves = 4;
-constexpr int kLThreads = kLWaves * kWave;
+constexpr int kLMaxParts = 8;
 
 struct LoraMatP {
     const uint16_t* a;
@@ -35,54 +34,75 @@ struct LoraParams {
     const int32_t* order;
     float* ws;
     int32_t count, groups, rows, x_rows, k, parts;
-    int32_t nblocks;  // expand: blocks of columns, the same for every matrix (the widest one's)
+    int32_t strips, strip_blocks;  // expand: strips of columns (the widest matrix's), blocks per strip
     int64_t block0;
 };
 
-__device__ __forceinline__ int lora_source(const LoraParams& p, int at) { return p.order[at]; }
+// ------------------------------------------------------------------ shrink
+// Eight waves; RT 16-row tiles of A (rank <= 16 RT).  A wave takes up to four
+// of them and a share of the part's k: waves that share tiles split k, and
+// their sums meet in LDS.
+constexpr int kSWaves = 8;
+constexpr int kSThreads = kSWaves * kWave;
 
-// RT: 16-row tiles of A (rank <= 16 RT)
 template <int RT>
 __device__ __forceinline__ void shrink_tile(const LoraParams& p, const LoraMatP& m, const RowTile& t, int kpart,
-                                            f32x4 (&red)[kLWaves][16][kWave]) {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+                                            f32x4 (&red)[kSWaves][4][kWave]) {
+    constexpr int RTW = RT < 4 ? RT : 4, RG = RT / RTW, KW = kSWaves / RG;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int units = p.k / 32, shares = p.parts * kLWaves, share = kpart * kLWaves + wave;
+    const int rg = wave / KW, share = kpart * KW + wave % KW, shares = p.parts * KW;
+    const int units = p.k / 32;
     const int c0 = (int)((int64_t)units * share / shares), c1 = (int)((int64_t)units * (share + 1) / shares);
-    const int src = min(max(lora_source(p, t.row0 + min(i, t.rows - 1)), 0), p.x_rows - 1);
+    const int src = min(max(p.order[t.row0 + min(i, t.rows - 1)], 0), p.x_rows - 1);
     const uint16_t* x = p.x + (int64_t)src * p.k + 8 * g;
-    const uint16_t* a[RT];
-    f32x4 acc[RT];
+    const uint16_t* a[RTW];
+    f32x4 acc[RTW];
 #pragma unroll
-    for (int q = 0; q < RT; ++q) {
-        a[q] = m.a + ((int64_t)t.group * m.r + min(16 * q + i, m.r - 1)) * p.k + 8 * g;
+    for (int q = 0; q < RTW; ++q) {
+        a[q] = m.a + ((int64_t)t.group * m.r + min(16 * (rg * RTW + q) + i, m.r - 1)) * p.k + 8 * g;
         acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    for (int c = c0; c < c1; ++c) {
-        const u32x4 xf = *reinterpret_cast<const u32x4*>(x + c * 32);
+    // the loads of several steps are requested together
+    auto batch = [&](int c, auto steps) {
+        constexpr int U = decltype(steps)::value;
+        u32x4 xf[U], af[U][RTW];
 #pragma unroll
-        for (int q = 0; q < RT; ++q) {
-            const u32x4 af = *reinterpret_cast<const u32x4*>(a[q] + c * 32);
-            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lbf16x8, af),
-                                                             __builtin_bit_cast(lbf16x8, xf), acc[q], 0, 0, 0);
+        for (int u = 0; u < U; ++u) {
+            xf[u] = *reinterpret_cast<const u32x4*>(x + (c + u) * 32);
+#pragma unroll
+            for (int q = 0; q < RTW; ++q) af[u][q] = *reinterpret_cast<const u32x4*>(a[q] + (c + u) * 32);
         }
-    }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int q = 0; q < RT; ++q) red[wave][q][lane] = acc[q];
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < RTW; ++q)
+                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lbf16x8, af[u][q]),
+                                                                 __builtin_bit_cast(lbf16x8, xf[u]), acc[q], 0, 0, 0);
+    };
+    constexpr int U = RTW == 4 ? 4 : 8;
+    int c = c0;
+    for (; c + U <= c1; c += U) batch(c, std::integral_constant<int, U>());
+    for (; c + 2 <= c1; c += 2) batch(c, std::integral_constant<int, 2>());
+    if (c < c1) batch(c, std::integral_constant<int, 1>());
+#pragma unroll
+    for (int q = 0; q < RTW; ++q) red[wave][q][lane] = acc[q];
     lds_barrier();
     const int rpad = (m.r + 15) / 16 * 16;
-    for (int q = wave; q < rpad / 16; q += kLWaves) {
-        f32x4 s = red[0][q][lane];
+    for (int q = wave; q < rpad / 16; q += kSWaves) {
+        f32x4 s = red[q / RTW * KW][q % RTW][lane];
 #pragma unroll
-        for (int w = 1; w < kLWaves; ++w) s += red[w][q][lane];
+        for (int w = 1; w < KW; ++w) s += red[q / RTW * KW + w][q % RTW][lane];
         // lane l: sorted row l % 16, ranks 16 q + 4 (l / 16) + r
         if (i < t.rows)
             *reinterpret_cast<f32x4*>(p.ws + m.ws_at + ((int64_t)kpart * p.rows + t.row0 + i) * rpad + 16 * q + 4 * g) = s;
     }
 }
 
-__global__ __launch_bounds__(kLThreads) void lora_shrink_kernel(LoraParams p) {
-    __shared__ f32x4 red[kLWaves][16][kWave];
+__global__ __launch_bounds__(kSThreads) void lora_shrink_kernel(LoraParams p) {
+    __shared__ f32x4 red[kSWaves][4][kWave];
     const int64_t block = p.block0 + blockIdx.x;
     const int mi = (int)(block % p.count), kpart = (int)(block / p.count % p.parts);
     const RowTile t = find_row_tile<16>(p.offsets, p.groups, p.rows, (int)(block / p.count / p.parts));
@@ -95,87 +115,255 @@ __global__ __launch_bounds__(kLThreads) void lora_shrink_kernel(LoraParams p) {
     else shrink_tile<16>(p, m, t, kpart, red);
 }
 
-constexpr int kLCols = 256;  // columns per expand workgroup: 4 waves x 4 tiles of 16
+// ------------------------------------------------------------------ expand
+// A workgroup takes 16 MT sorted rows of one adapter and a strip of blocks of
+// 64 CT columns of one matrix, each of its four waves all the rows and 16 CT
+// columns of a block.  v is summed, scaled and split once per strip; the old y
+// and B of a block are requested one block ahead; the products go through
+// LDS so that y is read and written in whole rows of 64 CT columns.
+constexpr int kXThreads = 256;
 
-template <int YT>
-__global__ __launch_bounds__(kLThreads) void lora_expand_kernel(LoraParams p) {
-    extern __shared__ u32x4 vsh[];  // [term][k group of 8][16 rows] bf16 x 8
+// y of many rows is read and written once: non-temporal (5% at 4129 x 11008).
+// The few rows of a decode step stay in the caches for the next kernel.
+template <bool NT, typename T>
+__device__ __forceinline__ T load_y(const T* p) {
+    return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void write_y(T v, T* p) {
+    if constexpr (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <int YT, int MT, int KC, int CT>
+__global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel(LoraParams p) {
+    constexpr int R = 16 * MT;                  // rows
+    constexpr int KG = 4 * KC;                  // k groups of 8
+    constexpr int kXCols = 64 * CT, kXLine = kXCols + 4;  // 4 floats longer: no bank conflicts
+    constexpr int TPR = kXCols / 4;             // threads per row of y, 4 columns each
+    constexpr int RPP = kXThreads / TPR;        // rows per pass of the workgroup
+    constexpr int YR = R / RPP;                 // passes
+    __shared__ u32x4 vsh[3 * KG * R];           // v: [term][k group of 8][row]
+    __shared__ __attribute__((aligned(16))) float dsh[R * kXLine];
     const int64_t block = p.block0 + blockIdx.x;
-    const int nb = (int)(block % p.nblocks), mi = (int)(block / p.nblocks % p.count);
+    const int strip = (int)(block % p.strips), mi = (int)(block / p.strips % p.count);
     const LoraMatP& m = p.m[mi];
-    if (nb * kLCols >= m.n) return;
-    const RowTile t = find_row_tile<16>(p.offsets, p.groups, p.rows, (int)(block / p.nblocks / p.count));
+    const int n = m.n, r = m.r;
+    const int nb1 = min((strip + 1) * p.strip_blocks, (n + kXCols - 1) / kXCols);
+    int nb = strip * p.strip_blocks;
+    if (nb >= nb1) return;
+    const RowTile t = find_row_tile<R>(p.offsets, p.groups, p.rows, (int)(block / p.strips / p.count));
     if (t.rows <= 0) return;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int rpad = (m.r + 15) / 16 * 16, kg = (m.r + 31) / 32 * 4;  // k groups of 8, whole matrix instructions
-    const float scale = m.scale ? m.scale[t.group] : 1.0f;
-    uint16_t* vh = reinterpret_cast<uint16_t*>(vsh);
-    for (int q = tid; q < kg * 8 * 16; q += kLThreads) {
-        const int row = q & 15, j = q >> 4;
-        float v = 0.0f;
-        if (j < m.r && row < t.rows) {
-            const float* at = p.ws + m.ws_at + (int64_t)(t.row0 + row) * rpad + j;
-            for (int s = 0; s < p.parts; ++s) v += at[(int64_t)s * p.rows * rpad];
-            v *= scale;
-        }
-        const uint32_t hi = f32_to_bf16(v);
-        const float v1 = v - bf16_to_f32(hi);
-        const uint32_t mid = f32_to_bf16(v1);
-        const uint32_t lo = f32_to_bf16(v1 - bf16_to_f32(mid));
-        const int slot = ((j >> 3) * 16 + row) * 8 + (j & 7);
-        vh[slot] = (uint16_t)hi;
-        vh[kg * 128 + slot] = (uint16_t)mid;
-        vh[2 * kg * 128 + slot] = (uint16_t)lo;
+    const bool vec = (n & 3) == 0;  // whole 4-column pieces, aligned
+
+    struct Block {
+        u32x4 b[CT][KC];
+        float y[YR][4];
+    };
+    // y: thread (row tid / TPR + RPP s, columns 4 (tid % TPR) .. + 3; one by one
+    // tid % TPR + TPR e where n is no multiple of 4)
+    const int ycol = tid % TPR;
+    int64_t yat[YR];
+#pragma unroll
+    for (int s = 0; s < YR; ++s) {
+        const int row = tid / TPR + RPP * s;
+        const int src = row < t.rows ? p.order[t.row0 + row] : -1;
+        yat[s] = src >= 0 && src < p.x_rows ? (int64_t)src * n : -1;
     }
-    lds_barrier();
-    const int trow = i < t.rows ? lora_source(p, t.row0 + i) : -1;
-    const bool live = trow >= 0 && trow < p.x_rows;
+    auto load = [&](int block_n, Block& k) {
+        const int n0 = block_n * kXCols;
+        // B: lane (i, g) holds column i of a 16-column tile, ranks 8 (4 c + g) .. + 7
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int n0 = nb * kLCols + (wave * 4 + q) * 16;
-        if (n0 >= m.n) break;
-        const uint16_t* b = m.b + ((int64_t)t.group * m.n + min(n0 + i, m.n - 1)) * m.r;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < kg; c += 4) {
-            u32x4 bf = {0u, 0u, 0u, 0u};
-            if ((c + g) * 8 < m.r) bf = *reinterpret_cast<const u32x4*>(b + (c + g) * 8);
+        for (int q = 0; q < CT; ++q) {
+            const uint16_t* b = m.b + ((int64_t)t.group * n + min(n0 + 16 * (wave * CT + q) + i, n - 1)) * r;
 #pragma unroll
-            for (int term = 0; term < 3; ++term)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(lbf16x8, bf),
-                    __builtin_bit_cast(lbf16x8, vsh[(term * kg + c + g) * 16 + i]), acc, 0, 0, 0);
+            for (int c = 0; c < KC; ++c) {
+                const int at = (4 * c + g) * 8;
+                k.b[q][c] = u32x4{0u, 0u, 0u, 0u};
+                if (at < r) k.b[q][c] = *reinterpret_cast<const u32x4*>(b + at);
+            }
         }
-        if (live) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int n = n0 + 4 * g + r;
-                if (n < m.n) {
-                    const int64_t at = (int64_t)trow * m.n + n;
+        for (int s = 0; s < YR; ++s) {
+            if (yat[s] < 0) continue;
+            if (vec) {
+                const int64_t at = yat[s] + n0 + 4 * ycol;
+                if (n0 + 4 * ycol < n) {
                     if constexpr (YT == 0) {
-                        float* y = static_cast<float*>(m.y);
-                        y[at] = y[at] + acc[r];
+                        const f32x4 v = load_y<MT != 1>(reinterpret_cast<const f32x4*>(static_cast<const float*>(m.y) + at));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) k.y[s][e] = v[e];
                     } else {
-                        uint16_t* y = static_cast<uint16_t*>(m.y);
-                        y[at] = (uint16_t)f32_to_bf16(bf16_to_f32(y[at]) + acc[r]);
+                        const u32x2 v = load_y<MT != 1>(reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(m.y) + at));
+                        k.y[s][0] = bf16_to_f32(v.x & 0xFFFFu);
+                        k.y[s][1] = __uint_as_float(v.x & 0xFFFF0000u);
+                        k.y[s][2] = bf16_to_f32(v.y & 0xFFFFu);
+                        k.y[s][3] = __uint_as_float(v.y & 0xFFFF0000u);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t at = yat[s] + n0 + ycol + TPR * e;
+                    if (n0 + ycol + TPR * e < n)
+                        k.y[s][e] = YT == 0 ? static_cast<const float*>(m.y)[at] : bf16_to_f32(static_cast<const uint16_t*>(m.y)[at]);
+                }
+            }
+        }
+    };
+    auto finish = [&](int block_n, const Block& k) {
+        const int n0 = block_n * kXCols;
+        f32x4 acc[MT][CT];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int q = 0; q < CT; ++q) acc[a][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int w = 0; w < 3; ++w)
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    const lbf16x8 v = __builtin_bit_cast(lbf16x8, vsh[(w * KG + 4 * c + g) * R + 16 * a + i]);
+#pragma unroll
+                    for (int q = 0; q < CT; ++q)
+                        acc[a][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lbf16x8, k.b[q][c]), v, acc[a][q], 0, 0, 0);
+                }
+        // lane l holds row 16 a + l % 16, columns 16 (CT wave + q) + 4 (l / 16) + r
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int q = 0; q < CT; ++q)
+                *reinterpret_cast<f32x4*>(dsh + (16 * a + i) * kXLine + 16 * (wave * CT + q) + 4 * g) = acc[a][q];
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < YR; ++s) {
+            if (yat[s] < 0) continue;
+            const float* line = dsh + (tid / TPR + RPP * s) * kXLine;
+            if (vec) {
+                const int64_t at = yat[s] + n0 + 4 * ycol;
+                if (n0 + 4 * ycol < n) {
+                    f32x4 v = *reinterpret_cast<const f32x4*>(line + 4 * ycol);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += k.y[s][e];
+                    if constexpr (YT == 0) {
+                        write_y<MT != 1>(v, reinterpret_cast<f32x4*>(static_cast<float*>(m.y) + at));
+                    } else {
+                        const u32x2 o = {f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16)};
+                        write_y<MT != 1>(o, reinterpret_cast<u32x2*>(static_cast<uint16_t*>(m.y) + at));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t at = yat[s] + n0 + ycol + TPR * e;
+                    if (n0 + ycol + TPR * e < n) {
+                        const float v = k.y[s][e] + line[ycol + TPR * e];
+                        if constexpr (YT == 0) static_cast<float*>(m.y)[at] = v;
+                        else static_cast<uint16_t*>(m.y)[at] = (uint16_t)f32_to_bf16(v);
                     }
                 }
             }
         }
+        lds_barrier();  // dsh is written again by the next block
+    };
+
+    Block ka, kb;
+    load(nb, ka);
+    __builtin_amdgcn_sched_barrier(0);
+    // v: the parts in order, scaled, as hi + mid + lo bf16 (24 bits), rows and
+    // ranks past the ends zero
+    const int rpad = (r + 15) / 16 * 16;
+    const float scale = m.scale ? m.scale[t.group] : 1.0f;
+    uint2* vh = reinterpret_cast<uint2*>(vsh);
+#pragma unroll
+    for (int q0 = 0; q0 < R * KC * 8; q0 += kXThreads) {
+        const int q = q0 + tid;
+        if (R * KC * 8 % kXThreads != 0 && q >= R * KC * 8) break;
+        const int j4 = q % (KC * 8), row = q / (KC * 8);
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (4 * j4 < r && row < t.rows) {
+            const float* at = p.ws + m.ws_at + (int64_t)(t.row0 + row) * rpad + 4 * j4;
+            const int64_t step = (int64_t)p.rows * rpad;
+            if (p.parts == 1) {
+                v = *reinterpret_cast<const f32x4*>(at);
+            } else {
+                f32x4 part[kLMaxParts];
+#pragma unroll
+                for (int s = 0; s < kLMaxParts; ++s) part[s] = *reinterpret_cast<const f32x4*>(at + min(s, p.parts - 1) * step);
+#pragma unroll
+                for (int s = 0; s < kLMaxParts; ++s)
+                    if (s < p.parts) v += part[s];
+            }
+        }
+        uint32_t term[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f = v[e] * scale;
+            term[0][e] = f32_to_bf16(f);
+            const float f1 = f - bf16_to_f32(term[0][e]);
+            term[1][e] = f32_to_bf16(f1);
+            term[2][e] = f32_to_bf16(f1 - bf16_to_f32(term[1][e]));
+        }
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+            vh[((w * KG + (j4 >> 1)) * R + row) * 2 + (j4 & 1)] =
+                make_uint2(term[w][0] | (term[w][1] << 16), term[w][2] | (term[w][3] << 16));
+    }
+    lds_barrier();
+    for (;;) {
+        if (nb + 1 < nb1) load(nb + 1, kb);
+        __builtin_amdgcn_sched_barrier(0);
+        finish(nb, ka);
+        if (++nb >= nb1) break;
+        if (nb + 1 < nb1) load(nb + 1, ka);
+        __builtin_amdgcn_sched_barrier(0);
+        finish(nb, kb);
+        if (++nb >= nb1) break;
     }
 }
 
-static int lora_parts(int64_t rows, int64_t groups, int64_t k) {
-    const int64_t tiles = max_row_tiles(rows, groups, 16);
-    int64_t parts = (512 + tiles - 1) / tiles;
-    const int64_t most = k / 32 / (2 * kLWaves);  // at least two matrix instructions deep per wave
+// Parts of k of the shrink: enough workgroups to fill the CUs.
+static int lora_parts(int64_t rows, int64_t groups, int64_t k, int count) {
+    const int64_t blocks = max_row_tiles(rows, groups, 16) * count;
+    int64_t parts = (256 + blocks - 1) / blocks;
+    const int64_t most = k / 32 / kSWaves;  // a matrix instruction per wave at least
     if (parts > most) parts = most;
-    if (parts > 16) parts = 16;
+    if (parts > kLMaxParts) parts = kLMaxParts;
     return (int)(parts < 1 ? 1 : parts);
 }
 
-size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int64_t padded_rank) {
-    return (size_t)lora_parts(rows, groups, k) * (size_t)rows * (size_t)padded_rank * sizeof(float);
+size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int count, int64_t padded_rank) {
+    return (size_t)lora_parts(rows, groups, k, count) * (size_t)rows * (size_t)padded_rank * sizeof(float);
+}
+
+template <int YT, int MT, int KC, int CT>
+static hipError_t run_expand(LoraParams& p, int64_t widest, hipStream_t st) {
+    const int64_t blocks = (widest + 64 * CT - 1) / (64 * CT), tiles = max_row_tiles(p.rows, p.groups, 16 * MT) * p.count;
+    // Strips as long as they can be with enough workgroups left (y of 4129 x
+    // 11008 fp32, rank 64: 512, 768, 1024, 4096 workgroups 155, 127, 121, 118
+    // us with the shrink; q, k, v of 61 rows: 1024 and 4096 18 and 20 us).
+    int64_t per = blocks * tiles / (MT == 1 ? 1024 : 4096);
+    per = per < 1 ? 1 : per > blocks ? blocks : per;
+    p.strip_blocks = (int32_t)per;
+    p.strips = (int32_t)((blocks + per - 1) / per);
+    return launch_blocks(tiles * p.strips, kXThreads, [&](uint32_t grid, int64_t block0) {
+        p.block0 = block0;
+        lora_expand_kernel<YT, MT, KC, CT><<<grid, kXThreads, 0, st>>>(p);
+    });
+}
+template <int YT>
+static hipError_t launch_expand(LoraParams& p, int rmax, int64_t widest, hipStream_t st) {
+    // 32 rows per workgroup where the groups have that many
+    const bool tall = p.rows >= 32 * (int64_t)p.groups;
+    if (rmax <= 32) return tall ? run_expand<YT, 2, 1, 2>(p, widest, st) : run_expand<YT, 1, 1, 4>(p, widest, st);
+    if (rmax <= 64) return tall ? run_expand<YT, 2, 2, 2>(p, widest, st) : run_expand<YT, 1, 2, 4>(p, widest, st);
+    if (rmax <= 128) return tall ? run_expand<YT, 2, 4, 1>(p, widest, st) : run_expand<YT, 1, 4, 2>(p, widest, st);
+    return tall ? run_expand<YT, 2, 8, 1>(p, widest, st) : run_expand<YT, 1, 8, 1>(p, widest, st);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t st) {
@@ -189,7 +377,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t st) {
     p.rows = (int32_t)a.rows;
     p.x_rows = (int32_t)a.x_rows;
     p.k = (int32_t)a.k;
-    p.parts = lora_parts(a.rows, a.groups, a.k);
+    p.parts = lora_parts(a.rows, a.groups, a.k, a.count);
     int64_t at = 0, widest = 0;
     int rmax = 0;
     for (int j = 0; j < a.count; ++j) {
@@ -199,19 +387,13 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t st) {
         if (m.n > widest) widest = m.n;
         if (m.r > rmax) rmax = m.r;
     }
-    const int64_t tiles = max_row_tiles(a.rows, a.groups, 16);
-    hipError_t e = launch_blocks(tiles * p.parts * p.count, kLThreads, [&](uint32_t grid, int64_t block0) {
-        p.block0 = block0;
-        lora_shrink_kernel<<<grid, kLThreads, 0, st>>>(p);
-    });
+    const hipError_t e = launch_blocks(max_row_tiles(a.rows, a.groups, 16) * p.parts * p.count, kSThreads,
+                                       [&](uint32_t grid, int64_t block0) {
+                                           p.block0 = block0;
+                                           lora_shrink_kernel<<<grid, kSThreads, 0, st>>>(p);
+                                       });
     if (e != hipSuccess) return e;
-    p.nblocks = (int32_t)((widest + kLCols - 1) / kLCols);
-    const size_t lds = (size_t)3 * ((rmax + 31) / 32 * 4) * 16 * sizeof(u32x4);
-    return launch_blocks(tiles * p.nblocks * p.count, kLThreads, [&](uint32_t grid, int64_t block0) {
-        p.block0 = block0;
-        if (a.yt == 0) lora_expand_kernel<0><<<grid, kLThreads, lds, st>>>(p);
-        else lora_expand_kernel<1><<<grid, kLThreads, lds, st>>>(p);
-    });
+    return a.yt == 0 ? launch_expand<0>(p, rmax, widest, st) : launch_expand<1>(p, rmax, widest, st);
 }
 
 }  // namespace qg
