@@ -715,19 +715,31 @@ def qgemm_w8a8(xq: torch.Tensor, s_x: torch.Tensor, x_out: Optional[torch.Tensor
 # ------------------------------------------------------------------ products whose matrix depends on the row
 
 def _same_device(x: torch.Tensor, *others: Optional[torch.Tensor]):
+    index = x.get_device()
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors are on %s and %s" % (x.device, t.device))
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent in builds without a GPU backend
 
 
 def _call(name: str, x: torch.Tensor, *args):
     """The entry point `name` on x's current stream (appended as the last
     argument), with x's device current for the launch."""
-    if x.device.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, _stream(x)), name)
+    index = x.get_device()
+    f = getattr(_lib or lib(), name)
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(x.device):
-            _check(getattr(lib(), name)(*args, _stream(x)), name)
+        with torch.cuda.device(index):
+            st = f(*args, _raw_stream(index))
+    if st != QG_OK:
+        raise QgError(st, name)
 
 
 def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor):
@@ -735,7 +747,7 @@ def _shaped(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tens
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     _same_device(like, t)
     return t
@@ -810,7 +822,7 @@ def group_rows(ids: torch.Tensor, groups: int, out: Optional[RowGroups] = None,
     rows = ids.numel()
     out = _plan_buffers(ids, rows, groups, 1, out)
     ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(rows, groups)), ids)
-    _call("qg_group_rows", ids, _p(ids), rows, groups, _p(out.offsets), _p(out.order), _p(out.pos), _p(ws), nws)
+    _call("qg_group_rows", ids, _ptr(ids), rows, groups, _ptr(out.offsets), _ptr(out.order), _ptr(out.pos), _ptr(ws), nws)
     return out
 
 
@@ -826,8 +838,8 @@ def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, out: Option
     weights = _shaped(None if out is None else out.weights, "out.weights", (t, top_k), torch.float32, logits)
     plan = _plan_buffers(logits, t * top_k, e, top_k, None if out is None else out.groups)
     ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(t * top_k, e)), logits)
-    _call("qg_moe_route", logits, _p(logits), _xt(logits), t, e, top_k, 1 if renorm else 0, _p(ids), _p(weights),
-          _p(plan.offsets), _p(plan.order), _p(plan.pos), _p(ws), nws)
+    _call("qg_moe_route", logits, _ptr(logits), _xt(logits), t, e, top_k, 1 if renorm else 0, _ptr(ids), _ptr(weights),
+          _ptr(plan.offsets), _ptr(plan.order), _ptr(plan.pos), _ptr(ws), nws)
     return Routing(ids, weights, plan) if out is None else out
 
 
@@ -918,7 +930,7 @@ def qgemm_experts(w: QExperts, x: torch.Tensor, groups: RowGroups, s_x: Optional
     amode = _experts_x(w, x, groups, s_x, gather)
     y = _shaped(y, "y", (groups.rows, w.n), _y_dtype(y, y_dtype), x)
     cg = groups.c_struct(gather)
-    _call("qg_qgemm_experts", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _p(x), _p(s_x), x.shape[0], _p(y),
+    _call("qg_qgemm_experts", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _ptr(x), _ptr(s_x), x.shape[0], _ptr(y),
           _xt(y))
     return y
 
@@ -933,7 +945,7 @@ def qgemm_experts_swiglu(gate: QExperts, up: QExperts, x: torch.Tensor, groups: 
     y = _shaped(y, "y", (groups.rows, gate.n), _y_dtype(y, y_dtype), x)
     cg = groups.c_struct(gather)
     _call("qg_qgemm_experts_swiglu", x, ctypes.byref(gate.c_struct()), ctypes.byref(up.c_struct()), ctypes.byref(cg),
-          amode, _p(x), _p(s_x), x.shape[0], _p(y), _xt(y))
+          amode, _ptr(x), _ptr(s_x), x.shape[0], _ptr(y), _xt(y))
     return y
 
 
@@ -952,8 +964,8 @@ def qgemm_experts_combine(w: QExperts, x: torch.Tensor, groups: RowGroups, weigh
     y = _shaped(y, "y", (tokens, w.n), _y_dtype(y, y_dtype), x)
     ws, nws = _workspace(ws, int(lib().qg_experts_combine_workspace_bytes(groups.rows, w.n)), x)
     cg = groups.c_struct(gather)
-    _call("qg_qgemm_experts_combine", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _p(x), _p(s_x), x.shape[0],
-          _p(groups.pos), _p(weights), tokens, _p(y), _xt(y), _p(ws), nws)
+    _call("qg_qgemm_experts_combine", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _ptr(x), _ptr(s_x), x.shape[0],
+          _ptr(groups.pos), _ptr(weights), tokens, _ptr(y), _xt(y), _ptr(ws), nws)
     return y
 
 
@@ -1021,7 +1033,7 @@ class LoraLaunch:
         self.ws, self.nws = _workspace(ws, int(lib().qg_lora_workspace_bytes(self.m, n, m, groups.groups, k)), x)
         self.cg = groups.c_struct()
         self.x, self.keep = x, (groups, list(adapters), list(ys))
-        self.args = (self.m, n, ctypes.byref(self.cg), _p(x), m, k, _xt(ys[0]), _p(self.ws), self.nws)
+        self.args = (self.m, n, ctypes.byref(self.cg), _ptr(x), m, k, _xt(ys[0]), _ptr(self.ws), self.nws)
 
     def launch(self):
         _call("qg_lora_add", self.x, *self.args)

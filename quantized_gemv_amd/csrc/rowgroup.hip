@@ -2,15 +2,23 @@
 // number (expert, adapter), and the top-k router that gives the numbers.
 //
 // Grouping is a stable counting sort of ids[rows] by id (ids outside
-// [0, groups) are dropped), in chunks of up to 64 workgroups:
+// [0, groups) are dropped), in chunks of consecutive rows:
 //   count: per chunk, how many ids of each group (LDS, integer);
 //   place: per chunk, base[g] = rows of smaller groups + rows of group g in
-//          earlier chunks; then blocks of 2048 ids in order.  Eight waves take
-//          256 consecutive ids each, 64 at a time: ids that are equal within
-//          the 64 find each other by ballots over the id's bits, so a row's
-//          place is its wave's base + earlier equal ids of the wave + equal
-//          lanes below.  Nothing depends on the order of atomics.
-// A single chunk counts inside the place kernel: one launch.
+//          earlier chunks (every workgroup adds up all chunks' counts); then
+//          blocks of ids in order.  Eight waves take consecutive ids each, 64
+//          at a time: ids that are equal within the 64 find each other by
+//          ballots over the id's bits, so a row's place is its wave's base +
+//          earlier equal ids of the wave + equal lanes below.
+// Sums of integers only: nothing depends on the order of the atomics.  Up to
+// kGSingle rows are one chunk, counted inside the place kernel: one launch.
+// The router counts its own choices (one launch less), and a decode step's
+// few tokens are routed and placed by one workgroup, in one launch.
+//
+// Latency bounds all of this.  Measured (MI355X, kernel times): 16 tokens of
+// 64 experts, top 8: 5.3 us in one launch (3.0 + 3.7 us as route and
+// place); 8192 tokens of 128 experts, top 8: 8.3 + 5.0 us (6.2 + 3.2 + 14.0 us with a
+// count kernel of its own and the counts added up one chunk after another).
 #include "qg_launch.h"
 #include "qg_rows.h"
 
@@ -18,9 +26,7 @@ namespace qg {
 
 constexpr int kGThreads = 512;
 constexpr int kGWaves = kGThreads / kWave;
-constexpr int kGSteps = 4;                             // 64 ids per wave and step
-constexpr int kGBlock = kGThreads * kGSteps;           // ids placed between two barriers
-constexpr int kGMaxChunks = 64;
+constexpr int kGSingle = 2048;  // rows that one workgroup counts and places by itself
 
 struct GroupParams {
     const int32_t* ids;
@@ -67,22 +73,26 @@ __device__ __forceinline__ int scan_groups(const int* total, int* base, int grou
 static_assert(kMaxRowGroups == 2 * kGThreads, "two groups per thread");
 
 // Places the ids [lo, hi): base[g] (LDS) is the next place of group g and is
-// advanced; whist is [kGWaves][groups] of LDS.
-template <typename Ids>
+// advanced; whist is [kGWaves][groups] of LDS.  S: steps of 64 ids per wave
+// between two barriers.
+template <int S, typename Ids>
 __device__ __forceinline__ void place_ids(const GroupParams& p, const Ids& id_at, int lo, int hi, int* base, int* whist) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
-    for (int b0 = lo; b0 < hi; b0 += kGBlock) {
+    for (int b0 = lo; b0 < hi; b0 += S * kGThreads) {
+        int id[S], rank[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int i = b0 + (w * S + s) * kWave + lane;
+            const int v = i < hi ? id_at(i) : -1;
+            id[s] = (uint32_t)v < (uint32_t)p.groups ? v : -1;
+        }
         for (int q = tid; q < kGWaves * p.groups; q += kGThreads) whist[q] = 0;
         lds_barrier();
-        int id[kGSteps], rank[kGSteps];
         volatile int* mine = whist + w * p.groups;
 #pragma unroll
-        for (int s = 0; s < kGSteps; ++s) {
-            const int i = b0 + (w * kGSteps + s) * kWave + lane;
-            const int v = i < hi ? id_at(i) : -1;
-            const bool live = (uint32_t)v < (uint32_t)p.groups;
-            id[s] = live ? v : -1;
+        for (int s = 0; s < S; ++s) {
+            const bool live = id[s] >= 0;
             uint64_t same = __ballot(live);
             for (int q = 0; q < p.bits; ++q) {
                 const uint64_t one = __ballot((id[s] >> q) & 1);
@@ -99,18 +109,20 @@ __device__ __forceinline__ void place_ids(const GroupParams& p, const Ids& id_at
         }
         lds_barrier();
         for (int g = tid; g < p.groups; g += kGThreads) {
-            int run = base[g];
+            int run = base[g], c[kGWaves];
+#pragma unroll
+            for (int q = 0; q < kGWaves; ++q) c[q] = whist[q * p.groups + g];
+#pragma unroll
             for (int q = 0; q < kGWaves; ++q) {
-                const int c = whist[q * p.groups + g];
                 whist[q * p.groups + g] = run;
-                run += c;
+                run += c[q];
             }
             base[g] = run;
         }
         lds_barrier();
 #pragma unroll
-        for (int s = 0; s < kGSteps; ++s) {
-            const int i = b0 + (w * kGSteps + s) * kWave + lane;
+        for (int s = 0; s < S; ++s) {
+            const int i = b0 + (w * S + s) * kWave + lane;
             if (i < hi) {
                 int at = -1;
                 if (id[s] >= 0) {
@@ -124,6 +136,59 @@ __device__ __forceinline__ void place_ids(const GroupParams& p, const Ids& id_at
     }
 }
 
+// All rows by one workgroup; total, base: [groups] of LDS.
+template <typename Ids>
+__device__ __forceinline__ void place_all(const GroupParams& p, const Ids& id_at, int* whist, int* base, int* total,
+                                          int* scratch) {
+    const int tid = threadIdx.x;
+    for (int g = tid; g < p.groups; g += kGThreads) total[g] = 0;
+    lds_barrier();
+    for (int i = tid; i < p.rows; i += kGThreads) {
+        const uint32_t id = (uint32_t)id_at(i);
+        if (id < (uint32_t)p.groups) atomicAdd(&total[id], 1);
+    }
+    lds_barrier();
+    const int all = scan_groups(total, base, p.groups, scratch);
+    for (int g = tid; g < p.groups; g += kGThreads) p.offsets[g] = base[g];
+    if (tid == 0) p.offsets[p.groups] = all;
+    for (int i = all + tid; i < p.rows; i += kGThreads) p.order[i] = -1;
+    lds_barrier();
+    if (p.rows <= kGThreads) place_ids<1>(p, id_at, 0, p.rows, base, whist);
+    else place_ids<4>(p, id_at, 0, p.rows, base, whist);
+}
+
+// total[g] and before[g] += the counts of all chunks and of those before this
+// workgroup's: a thread adds W consecutive groups of every cs-th chunk.
+template <int W>
+__device__ __forceinline__ void sum_counts(const GroupParams& p, int* total, int* before) {
+    typedef int vec __attribute__((ext_vector_type(W)));
+    constexpr int U = 8;  // loads in flight
+    const int units = p.groups / W, across = min(units, kGThreads), cs = kGThreads / across;
+    const int c0 = (int)threadIdx.x / across;
+    if (c0 >= cs) return;
+    for (int u = (int)threadIdx.x % across; u < units; u += across) {
+        const int32_t* at = p.counts + u * W;
+        vec all = 0, mine = 0;
+        for (int c = c0; c < p.chunks; c += U * cs) {
+            vec v[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] = *reinterpret_cast<const vec*>(at + (int64_t)min(c + q * cs, p.chunks - 1) * p.groups);
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                if (c + q * cs < p.chunks) all += v[q];
+                if (c + q * cs < (int)blockIdx.x) mine += v[q];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            atomicAdd(&total[u * W + e], all[e]);
+            atomicAdd(&before[u * W + e], mine[e]);
+        }
+    }
+}
+
+inline size_t group_lds(int groups) { return (size_t)(kGWaves + 2) * groups * sizeof(int); }
+
 __global__ __launch_bounds__(kGThreads) void group_place_kernel(GroupParams p) {
     extern __shared__ int lds[];  // whist [kGWaves][groups] | base [groups] | total [groups]
     __shared__ int scratch[kGWaves];
@@ -131,71 +196,71 @@ __global__ __launch_bounds__(kGThreads) void group_place_kernel(GroupParams p) {
     int* base = lds + kGWaves * p.groups;
     int* total = base + p.groups;
     const int tid = threadIdx.x;
-    const int lo = blockIdx.x * p.chunk, hi = min(lo + p.chunk, p.rows);
+    auto id_at = [&](int i) { return p.ids[i]; };
     if (p.chunks == 1) {
-        for (int g = tid; g < p.groups; g += kGThreads) total[g] = 0;
-        lds_barrier();
-        for (int i = tid; i < p.rows; i += kGThreads) {
-            const uint32_t id = (uint32_t)p.ids[i];
-            if (id < (uint32_t)p.groups) atomicAdd(&total[id], 1);
-        }
-        lds_barrier();
-        const int all = scan_groups(total, base, p.groups, scratch);
+        place_all(p, id_at, whist, base, total, scratch);
+        return;
+    }
+    // counts of all chunks, and of the chunks before this one (in whist, which
+    // place_ids clears again)
+    int* before = whist;
+    for (int g = tid; g < p.groups; g += kGThreads) total[g] = before[g] = 0;
+    lds_barrier();
+    if (p.groups % 4 == 0) sum_counts<4>(p, total, before);
+    else sum_counts<1>(p, total, before);
+    lds_barrier();
+    const int all = scan_groups(total, base, p.groups, scratch);
+    if (blockIdx.x == 0) {
         for (int g = tid; g < p.groups; g += kGThreads) p.offsets[g] = base[g];
         if (tid == 0) p.offsets[p.groups] = all;
-        for (int i = all + tid; i < p.rows; i += kGThreads) p.order[i] = -1;
-    } else {
-        for (int g = tid; g < p.groups; g += kGThreads) {
-            int t = 0;
-            for (int c = 0; c < p.chunks; ++c) t += p.counts[(int64_t)c * p.groups + g];
-            total[g] = t;
-        }
-        lds_barrier();
-        const int all = scan_groups(total, base, p.groups, scratch);
-        if (blockIdx.x == 0) {
-            for (int g = tid; g < p.groups; g += kGThreads) p.offsets[g] = base[g];
-            if (tid == 0) p.offsets[p.groups] = all;
-        }
-        lds_barrier();
-        for (int g = tid; g < p.groups; g += kGThreads) {
-            int t = base[g];
-            for (int c = 0; c < (int)blockIdx.x; ++c) t += p.counts[(int64_t)c * p.groups + g];
-            base[g] = t;
-        }
-        for (int i = max(all, lo) + tid; i < hi; i += kGThreads) p.order[i] = -1;
-        lds_barrier();
     }
-    place_ids(p, [&](int i) { return p.ids[i]; }, lo, hi, base, whist);
+    lds_barrier();
+    for (int g = tid; g < p.groups; g += kGThreads) base[g] += before[g];
+    const int lo = min((int)blockIdx.x * p.chunk, p.rows), hi = min(lo + p.chunk, p.rows);
+    for (int i = max(all, lo) + tid; i < hi; i += kGThreads) p.order[i] = -1;
+    lds_barrier();
+    if (p.chunk <= kGThreads) place_ids<1>(p, id_at, lo, hi, base, whist);
+    else place_ids<4>(p, id_at, lo, hi, base, whist);
 }
 
-static void group_chunks(int64_t rows, int32_t* chunk, int32_t* chunks) {
-    const int64_t blocks = (rows + kGBlock - 1) / kGBlock;
-    const int64_t per = (blocks + kGMaxChunks - 1) / kGMaxChunks;
-    *chunk = (int32_t)(per * kGBlock);
-    *chunks = (int32_t)((blocks + per - 1) / per);
+// Chunks at most: every workgroup of the place kernel reads all their counts.
+static int64_t max_chunks(int64_t groups) {
+    const int64_t c = 32768 / groups;
+    return c < 16 ? 16 : c > 256 ? 256 : c;
+}
+// Rows per chunk, a multiple of `unit`, at least `least`.
+static void group_chunks(int64_t rows, int64_t groups, int64_t unit, int64_t least, int32_t* chunk, int32_t* chunks) {
+    if (rows <= kGSingle) least = rows;
+    int64_t per = (rows + max_chunks(groups) - 1) / max_chunks(groups);
+    if (per < least) per = least;
+    per = (per + unit - 1) / unit * unit;
+    *chunk = (int32_t)per;
+    *chunks = (int32_t)((rows + per - 1) / per);
 }
 
 size_t group_workspace(int64_t rows, int64_t groups) {
-    int32_t chunk, chunks;
-    group_chunks(rows, &chunk, &chunks);
-    return chunks > 1 ? (size_t)chunks * (size_t)groups * sizeof(int32_t) : 0;
+    return rows > kGSingle ? (size_t)max_chunks(groups) * (size_t)groups * sizeof(int32_t) : 0;
 }
 
-hipError_t launch_group_rows(const GroupArgs& a, hipStream_t st) {
+static GroupParams group_params(const GroupArgs& a) {
     GroupParams p;
     p.ids = a.ids;
     p.rows = (int32_t)a.rows;
     p.groups = a.groups;
-    group_chunks(a.rows, &p.chunk, &p.chunks);
     p.bits = 0;
     while ((1 << p.bits) < a.groups) ++p.bits;
     p.offsets = a.offsets;
     p.order = a.order;
     p.pos = a.pos;
     p.counts = static_cast<int32_t*>(a.ws);
+    return p;
+}
+
+hipError_t launch_group_rows(const GroupArgs& a, hipStream_t st) {
+    GroupParams p = group_params(a);
+    group_chunks(a.rows, a.groups, 1, kGThreads, &p.chunk, &p.chunks);
     if (p.chunks > 1) group_count_kernel<<<p.chunks, kGThreads, 0, st>>>(p);
-    const size_t lds = (size_t)(kGWaves + 2) * a.groups * sizeof(int);
-    group_place_kernel<<<p.chunks, kGThreads, lds, st>>>(p);
+    group_place_kernel<<<p.chunks, kGThreads, group_lds(a.groups), st>>>(p);
     return hipGetLastError();
 }
 
@@ -230,20 +295,21 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 }
 
 template <int XT, int NJ>
-__device__ __forceinline__ void route_token(const void* logits, int64_t t, int experts, int top_k, bool renorm,
-                                            int& my_id, float& my_w) {
+__device__ __forceinline__ void load_keys(const void* logits, int64_t t, int experts, uint32_t (&key)[NJ]) {
     const int lane = threadIdx.x & (kWave - 1);
-    uint32_t key[NJ];
+    float l[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        const int e = lane + kWave * j;
-        key[j] = 0;
-        if (e < experts) {
-            const int64_t at = t * experts + e;
-            key[j] = logit_key(XT == 0 ? static_cast<const float*>(logits)[at]
-                                       : bf16_to_f32(static_cast<const uint16_t*>(logits)[at]));
-        }
+        const int64_t at = t * experts + min(lane + kWave * j, experts - 1);
+        l[j] = XT == 0 ? static_cast<const float*>(logits)[at] : bf16_to_f32(static_cast<const uint16_t*>(logits)[at]);
     }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = lane + kWave * j < experts ? logit_key(l[j]) : 0u;
+}
+
+template <int NJ>
+__device__ __forceinline__ void route_token(uint32_t (&key)[NJ], int top_k, bool renorm, int& my_id, float& my_w) {
+    const int lane = threadIdx.x & (kWave - 1);
     uint32_t best = key[0];
 #pragma unroll
     for (int j = 1; j < NJ; ++j) best = max(best, key[j]);
@@ -285,50 +351,109 @@ __device__ __forceinline__ void route_token(const void* logits, int64_t t, int e
     if (my_id >= 0) my_w = my_w / all;
 }
 
+constexpr int kRouteSmall = 64;  // tokens that one workgroup routes and places
+
 struct RouteParams {
     const void* logits;
-    int32_t tokens, experts, top_k, renorm;
+    int32_t tokens, top_k, renorm, per;  // per: tokens of a workgroup
     int32_t* ids;
     float* weights;
+    GroupParams g;
 };
 
-template <int XT, int NJ>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteParams p) {
+// Tokens lo + w, lo + w + waves, ... below hi by wave w, the next one's logits
+// requested before the choice; keep(pair, id) takes the choices.
+template <int XT, int NJ, typename Keep>
+__device__ __forceinline__ void route_tokens(const RouteParams& p, int lo, int hi, int waves, const Keep& keep) {
     const int lane = threadIdx.x & (kWave - 1);
-    const int t = blockIdx.x * kWaves + (int)threadIdx.x / kWave;
-    if (t >= p.tokens) return;
-    int id;
-    float w;
-    route_token<XT, NJ>(p.logits, t, p.experts, p.top_k, p.renorm != 0, id, w);
-    if (lane < p.top_k) {
-        p.ids[(int64_t)t * p.top_k + lane] = id;
-        p.weights[(int64_t)t * p.top_k + lane] = w;
+    int t = lo + (int)threadIdx.x / kWave;
+    if (t >= hi) return;
+    uint32_t key[NJ];
+    load_keys<XT, NJ>(p.logits, t, p.g.groups, key);
+    for (;;) {
+        const int next = t + waves;
+        uint32_t ahead[NJ];
+        load_keys<XT, NJ>(p.logits, min(next, hi - 1), p.g.groups, ahead);
+        int id;
+        float w;
+        route_token<NJ>(key, p.top_k, p.renorm != 0, id, w);
+        if (lane < p.top_k) {
+            const int64_t at = (int64_t)t * p.top_k + lane;
+            p.ids[at] = id;
+            p.weights[at] = w;
+            keep((int)at, id);
+        }
+        if (next >= hi) break;
+        t = next;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) key[j] = ahead[j];
     }
 }
 
+// A chunk of tokens per workgroup, the choices counted (unless the place
+// kernel's only workgroup counts them).
+constexpr int kRWaves = 16, kRThreads = kRWaves * kWave;
+
+template <int XT, int NJ>
+__global__ __launch_bounds__(kRThreads) void route_kernel(RouteParams p) {
+    __shared__ int hist[kMaxRowGroups];
+    for (int g = threadIdx.x; g < p.g.groups; g += kRThreads) hist[g] = 0;
+    lds_barrier();
+    const int lo = (int)blockIdx.x * p.per, hi = min(lo + p.per, p.tokens);
+    route_tokens<XT, NJ>(p, lo, hi, kRWaves, [&](int, int id) {
+        if (id >= 0) atomicAdd(&hist[id], 1);
+    });
+    if (p.g.chunks == 1) return;
+    lds_barrier();
+    for (int g = threadIdx.x; g < p.g.groups; g += kRThreads)
+        p.g.counts[(int64_t)blockIdx.x * p.g.groups + g] = hist[g];
+}
+
+// Few tokens: routed and placed by one workgroup.
+template <int XT, int NJ>
+__global__ __launch_bounds__(kGThreads) void route_small_kernel(RouteParams p) {
+    extern __shared__ int lds[];
+    __shared__ int scratch[kGWaves];
+    __shared__ int ids[kGSingle];
+    route_tokens<XT, NJ>(p, 0, p.tokens, kGWaves, [&](int at, int id) { ids[at] = id; });
+    lds_barrier();
+    int* base = lds + kGWaves * p.g.groups;
+    place_all(p.g, [&](int i) { return ids[i]; }, lds, base, base + p.g.groups, scratch);
+}
+
+template <int XT, int NJ>
+static void run_route(const RouteParams& p, hipStream_t st) {
+    const size_t lds = group_lds(p.g.groups);
+    if (p.per == 0) {
+        route_small_kernel<XT, NJ><<<1, kGThreads, lds, st>>>(p);
+    } else {
+        route_kernel<XT, NJ><<<(p.tokens + p.per - 1) / p.per, kRThreads, 0, st>>>(p);
+        group_place_kernel<<<p.g.chunks, kGThreads, lds, st>>>(p.g);
+    }
+}
 template <int XT>
 static void run_route(const RouteParams& p, hipStream_t st) {
-    const int grid = (p.tokens + kWaves - 1) / kWaves;
-    if (p.experts <= 64) route_kernel<XT, 1><<<grid, kThreads, 0, st>>>(p);
-    else if (p.experts <= 128) route_kernel<XT, 2><<<grid, kThreads, 0, st>>>(p);
-    else if (p.experts <= 256) route_kernel<XT, 4><<<grid, kThreads, 0, st>>>(p);
-    else route_kernel<XT, 16><<<grid, kThreads, 0, st>>>(p);
+    if (p.g.groups <= 64) run_route<XT, 1>(p, st);
+    else if (p.g.groups <= 128) run_route<XT, 2>(p, st);
+    else if (p.g.groups <= 256) run_route<XT, 4>(p, st);
+    else run_route<XT, 16>(p, st);
 }
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t st) {
     RouteParams p;
     p.logits = a.logits;
     p.tokens = (int32_t)a.tokens;
-    p.experts = a.group.groups;
     p.top_k = a.top_k;
     p.renorm = a.renorm;
     p.ids = a.ids;
     p.weights = a.weights;
+    p.g = group_params(a.group);
+    // whole tokens per chunk, at least one per wave
+    group_chunks(a.group.rows, a.group.groups, a.top_k, (int64_t)kRWaves * a.top_k, &p.g.chunk, &p.g.chunks);
+    p.per = p.g.chunks > 1 ? p.g.chunk / a.top_k : a.tokens > kRouteSmall ? kRWaves : 0;
     if (a.xt == 0) run_route<0>(p, st);
     else run_route<1>(p, st);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    return launch_group_rows(a.group, st);
+    return hipGetLastError();
 }
 
 }  // namespace qg
