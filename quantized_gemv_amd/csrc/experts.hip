@@ -14,7 +14,7 @@ namespace qg {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kEUnit = 64;  // k per unit: 4 lane groups x 16 codes
-constexpr int kEThreads = 512;
+constexpr int kEThreads = 256;
 constexpr int kEWaves = kEThreads / kWave;
 
 struct ExpertParams {
@@ -27,11 +27,9 @@ struct ExpertParams {
     void* y;
     int64_t expert_bytes;     // one expert's codes
     int32_t e, n, k, rows, x_rows, per_row;
-    int32_t row_stride, unit_stride, group_stride;  // bytes from row to row of a tile, unit to unit, k group to k group
     int32_t tiled;            // 16-row tiled codes (else row-major); a 16-row tile is 16 k bytes in both
     int64_t block0;           // workgroups of earlier launches of the same product
     int32_t ntiles;           // workgroup tiles along n
-    int32_t split;            // waves of a workgroup that share a tile, each with a part of k
 };
 
 // 16 int8 codes -> two bf16x8 (codes 0-7, 8-15), exact: fp32 by integer
@@ -60,83 +58,125 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
     else static_cast<uint16_t*>(y)[at] = (uint16_t)f32_to_bf16(v);
 }
 
-// Sixteen sorted rows of one expert times NT 16-row tiles of its matrix (GLU:
-// NT / 2 tiles of the gate and the same of the up matrix) per wave; the
-// workgroup's 8 waves take 8 / split groups of tiles and split parts of k
-// each, summed through LDS in order.
-template <int ACT, int YT, bool GLU>
+// ------------------------------------------------------------------ streams
+// Few rows per expert: the time goes into reading the chosen experts' codes.
+// A workgroup multiplies sixteen sorted rows of one expert with 32 matrix
+// rows (GLU: 16 of the gate and the same 16 of the up matrix); each of its
+// four waves takes a quarter of k, two 16 x 16 tiles of
+// v_mfma_f32_16x16x32_bf16 (or v_mfma_i32_16x16x64_i8) that share the x
+// fragments, and their sums meet in LDS in order.  A unit of 64 k is loaded
+// while the one before it is multiplied, and the first codes are requested
+// before the rows of x are known.  Quarters start at whole 128-byte lines of
+// row-major codes; tiled codes are read as whole blocks, once each:
+// non-temporal.
+//
+// HBM bounds it.  Small workgroups with little in registers keep the most of
+// them on a CU, so that one's start (tile search, row numbers) and end hide
+// behind the others' loads.  Waves per workgroup x tiles per wave x units per
+// step, us of the four cases with few rows (180, 237, 119 and 94 MB of codes):
+// 4 x 2 x 1: 32.5, 32.8, 24.6, 25.0; 4 x 4 x 2: 34.1, 36.3, 26.1, 25.0;
+// 8 x 4 x 2: 35.7, 45.0, 30.9, 29.2; 2 x 2 x 1: 33.9, 33.0, 25.0, 26.1.
+template <int ACT, int YT, bool GLU, bool TILED>
 __global__ __launch_bounds__(kEThreads) void experts_stream_kernel(ExpertParams p) {
-    constexpr int NT = 4;
-    constexpr int OT = GLU ? NT / 2 : NT;  // 16-row output tiles
+    constexpr int NT = 2;
+    constexpr int OT = GLU ? 1 : NT;      // 16-row output tiles
+    constexpr int XF = ACT == 0 ? 2 : 1;  // x loads per unit
     typedef typename std::conditional<ACT == 0, f32x4, i32x4>::type acc_t;
     __shared__ acc_t part[kEWaves][NT][kWave];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;  // weight row / x row, k group
     const int64_t block = p.block0 + blockIdx.x;
-    const int nt = (int)(block % p.ntiles);
+    const int ot0 = (int)(block % p.ntiles) * OT;  // first 16-row output tile
     const RowTile t = find_row_tile<16>(p.offsets, p.e, p.rows, (int)(block / p.ntiles));
     if (t.rows <= 0) return;  // uniform over the workgroup
 
-    // this lane's x row (rows past the tile repeat its last)
-    auto source = [&](int r) {
-        const int at = t.row0 + min(r, t.rows - 1);
-        const int src = p.order ? p.order[at] / p.per_row : at;
-        return min(max(src, 0), p.x_rows - 1);
-    };
-    const int src = source(i);
-    const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + (int64_t)src * p.k * (ACT == 0 ? 2 : 1) + (ACT == 0 ? 32 : 16) * g;
-
-    const int part_k = wave % p.split, grp = wave / p.split;
-    const int ot0 = (nt * (kEWaves / p.split) + grp) * OT;  // first 16-row output tile
-    const int units = p.k / kEUnit;
-    const int c0 = (int)((int64_t)units * part_k / p.split), c1 = (int)((int64_t)units * (part_k + 1) / p.split);
-
-    const int8_t* wrow[NT];
+    const int pairs = p.k / (2 * kEUnit);
+    const int c0 = 2 * (pairs * wave / kEWaves), c1 = 2 * (pairs * (wave + 1) / kEWaves);
+    __amdgpu_buffer_rsrc_t rw[NT];
+    uint32_t woff[NT];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
         // rows past n: row-major codes repeat the last row; tiled codes are
-        // padded to whole tiles, tiles past the last repeat it
+        // padded to whole tiles; tiles past the last repeat it
         const int ot = min(ot0 + q % OT, (p.n - 1) / 16);
-        const int row = p.tiled ? i : min(i, p.n - 1 - 16 * ot);
-        wrow[q] = p.codes[GLU ? q / OT : 0] + (int64_t)t.group * p.expert_bytes + (int64_t)ot * 16 * p.k +
-                  (int64_t)row * p.row_stride + g * p.group_stride;
+        rw[q] = make_rsrc(p.codes[GLU ? q : 0] + (int64_t)t.group * p.expert_bytes + (int64_t)ot * 16 * p.k,
+                          (uint32_t)(16 * p.k));
+        woff[q] = TILED ? (uint32_t)(lane * 16) : (uint32_t)(min(i, p.n - 1 - 16 * ot) * p.k + g * 16);
     }
+    struct Unit {
+        u32x4 w[NT], x[XF];
+    };
+    auto load_w = [&](int c, Unit& s) {
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+            s.w[q] = __builtin_amdgcn_raw_buffer_load_b128(rw[q], woff[q], c * (TILED ? 1024 : 64), TILED ? kCachePolicyNT : 0);
+    };
+    Unit sa, sb;
+    if (c0 < c1) load_w(c0, sa);
+    __builtin_amdgcn_sched_barrier(0);
+    // this lane's x row (rows past the tile repeat its last)
+    const int at = t.row0 + min(i, t.rows - 1);
+    const int src = min(max(p.order ? p.order[at] / p.per_row : at, 0), p.x_rows - 1);
+    const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + (int64_t)src * p.k * (ACT == 0 ? 2 : 1) + (ACT == 0 ? 32 : 16) * g;
+    auto load_x = [&](int c, Unit& s) {
+#pragma unroll
+        for (int f = 0; f < XF; ++f)
+            s.x[f] = *reinterpret_cast<const u32x4*>(xrow + (int64_t)c * (ACT == 0 ? 128 : 64) + 16 * f);
+    };
     acc_t acc[NT];
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[q] = acc_t{0, 0, 0, 0};
-    for (int c = c0; c < c1; ++c) {
-        u32x4 w[NT];
+    auto multiply = [&](const Unit& s) {
 #pragma unroll
-        for (int q = 0; q < NT; ++q) w[q] = *reinterpret_cast<const u32x4*>(wrow[q] + (int64_t)c * p.unit_stride);
-        if constexpr (ACT == 0) {
-            const u32x4 xa = *reinterpret_cast<const u32x4*>(xrow + (int64_t)c * 128);
-            const u32x4 xb = *reinterpret_cast<const u32x4*>(xrow + (int64_t)c * 128 + 16);
-#pragma unroll
-            for (int q = 0; q < NT; ++q) {
+        for (int q = 0; q < NT; ++q) {
+            if constexpr (ACT == 0) {
                 bf16x8 a0, a1;
-                codes_to_bf16(w[q], a0, a1);
-                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, xa), acc[q], 0, 0, 0);
-                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, xb), acc[q], 0, 0, 0);
+                codes_to_bf16(s.w[q], a0, a1);
+                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, s.x[0]), acc[q], 0, 0, 0);
+                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, s.x[XF - 1]), acc[q], 0, 0, 0);
+            } else {
+                acc[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, s.w[q]),
+                                                               __builtin_bit_cast(i32x4, s.x[0]), acc[q], 0, 0, 0);
             }
-        } else {
-            const i32x4 xa = *reinterpret_cast<const i32x4*>(xrow + (int64_t)c * 64);
-#pragma unroll
-            for (int q = 0; q < NT; ++q)
-                acc[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[q]), xa, acc[q], 0, 0, 0);
+        }
+    };
+    if (c0 < c1) {
+        load_x(c0, sa);
+        // a quarter holds whole pairs of units
+        for (int c = c0; c < c1; c += 2) {
+            load_w(c + 1, sb);
+            load_x(c + 1, sb);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(sa);
+            __builtin_amdgcn_sched_barrier(0);
+            if (c + 2 < c1) {
+                load_w(c + 2, sa);
+                load_x(c + 2, sa);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(sb);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (p.split > 1) {
+    // this lane's row scales, on their way while the quarters meet
+    float sw[NT][4];
+    if (wave == 0) {
 #pragma unroll
-        for (int q = 0; q < NT; ++q) part[wave][q][lane] = acc[q];
-        lds_barrier();
-        if (part_k != 0) return;
-        for (int w = 1; w < p.split; ++w)
+        for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int q = 0; q < NT; ++q) acc[q] += part[wave + w][q][lane];
+            for (int r = 0; r < 4; ++r)
+                sw[q][r] = p.scale[GLU ? q : 0][(int64_t)t.group * p.n + min(16 * (ot0 + q % OT) + 4 * g + r, p.n - 1)];
     }
+#pragma unroll
+    for (int q = 0; q < NT; ++q) part[wave][q][lane] = acc[q];
+    lds_barrier();
     // lane l holds x row l % 16, matrix rows 4 (l / 16) + r
-    if (i >= t.rows) return;
+    if (wave != 0 || i >= t.rows) return;
+#pragma unroll
+    for (int w = 1; w < kEWaves; ++w)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[q] += part[w][q][lane];
     const float sx = ACT == 0 ? 1.0f : p.s_x[src];
 #pragma unroll
     for (int q = 0; q < OT; ++q) {
@@ -144,10 +184,9 @@ __global__ __launch_bounds__(kEThreads) void experts_stream_kernel(ExpertParams 
         for (int r = 0; r < 4; ++r) {
             const int n = 16 * (ot0 + q) + 4 * g + r;
             if (n < p.n) {
-                const int64_t sw = (int64_t)t.group * p.n + n;
-                float o = (float)acc[q][r] / (ACT == 0 ? p.scale[0][sw] : p.scale[0][sw] * sx);
+                float o = (float)acc[q][r] / (ACT == 0 ? sw[q][r] : sw[q][r] * sx);
                 if constexpr (GLU) {
-                    const float u = (float)acc[OT + q][r] / (ACT == 0 ? p.scale[1][sw] : p.scale[1][sw] * sx);
+                    const float u = (float)acc[1][r] / (ACT == 0 ? sw[1][r] : sw[1][r] * sx);
                     o = swiglu(o, u);
                 }
                 store_y<YT>(p.y, (int64_t)(t.row0 + i) * p.n + n, o);
@@ -156,15 +195,13 @@ __global__ __launch_bounds__(kEThreads) void experts_stream_kernel(ExpertParams 
     }
 }
 
-template <int ACT, int YT, bool GLU>
+template <int ACT, int YT, bool GLU, bool TILED>
 static hipError_t run_stream(ExpertParams p, hipStream_t st) {
-    const int out_tiles = (p.n + 15) / 16, per_wave = GLU ? 2 : 4;
-    p.split = 8;
-    const int per_wg = per_wave * (kEWaves / p.split);
-    p.ntiles = (out_tiles + per_wg - 1) / per_wg;
+    const int out_tiles = (p.n + 15) / 16;
+    p.ntiles = GLU ? out_tiles : (out_tiles + 1) / 2;
     return launch_blocks(max_row_tiles(p.rows, p.e, 16) * p.ntiles, kEThreads, [&](uint32_t grid, int64_t block0) {
         p.block0 = block0;
-        experts_stream_kernel<ACT, YT, GLU><<<grid, kEThreads, 0, st>>>(p);
+        experts_stream_kernel<ACT, YT, GLU, TILED><<<grid, kEThreads, 0, st>>>(p);
     });
 }
 
@@ -411,7 +448,8 @@ template <int ACT, int YT, bool GLU>
 static hipError_t run_kind(const ExpertParams& p, hipStream_t st) {
     // the tile kernel keeps 32-bit offsets into x and a tile's y
     const bool small = (int64_t)p.x_rows * p.k * (ACT == 0 ? 2 : 1) < ((int64_t)1 << 32) && p.n < (1 << 21);
-    if (p.rows <= 16 * (int64_t)p.e || !small) return run_stream<ACT, YT, GLU>(p, st);
+    if (p.rows <= 16 * (int64_t)p.e || !small)
+        return p.tiled ? run_stream<ACT, YT, GLU, true>(p, st) : run_stream<ACT, YT, GLU, false>(p, st);
     return p.tiled ? run_tile<ACT, YT, GLU, true>(p, st) : run_tile<ACT, YT, GLU, false>(p, st);
 }
 template <int ACT, int YT>
@@ -438,54 +476,85 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t st) {
     p.per_row = a.per_row;
     p.expert_bytes = a.t16 ? (a.n + 15) / 16 * 16 * a.k : a.n * a.k;
     p.tiled = a.t16;
-    p.row_stride = a.t16 ? 16 : (int32_t)a.k;
-    p.unit_stride = a.t16 ? 1024 : 64;
-    p.group_stride = a.t16 ? 256 : 16;
     const bool glu = a.codes2 != nullptr;
     if (a.act_int8) return a.yt == 0 ? run_glu<1, 0>(p, glu, st) : run_glu<1, 1>(p, glu, st);
     return a.yt == 0 ? run_glu<0, 0>(p, glu, st) : run_glu<0, 1>(p, glu, st);
 }
 
 // ------------------------------------------------------------------ combine
-// One workgroup per token and 1024 outputs; a thread adds its 4 outputs over
-// the token's slots in slot order (fp32), so the result does not depend on
-// the plan's order.
+// A thread adds four consecutive outputs of a token over its slots, in slot
+// order (fp32), so the result does not depend on the plan's order; the rows of
+// up to eight slots are requested together.
 struct CombineParams {
     CombineArgs a;
     int64_t nblocks, block0;
+    int32_t cols;  // columns of a workgroup
 };
-template <int YT>
+template <int YT, bool VEC>
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
+    constexpr int S = 8;
     const CombineArgs& a = p.a;
     const int64_t block = p.block0 + blockIdx.x;
     const int64_t t = block / p.nblocks;
-    const int64_t n0 = (block % p.nblocks) * (4 * kThreads) + threadIdx.x;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < a.top_k; ++j) {
-        const int64_t at = a.pos[t * a.top_k + j];
-        if (at < 0 || at >= a.rows) continue;
-        const float w = a.weights[t * a.top_k + j];
+    const int64_t n0 = (block % p.nblocks) * p.cols + 4 * (int)threadIdx.x;
+    if (n0 >= a.n) return;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < a.top_k; j0 += S) {
+        f32x4 h[S];
+        float w[S];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t n = n0 + q * kThreads;
-            if (n < a.n) s[q] = __builtin_fmaf(w, a.h[at * a.n + n], s[q]);
+        for (int j = 0; j < S; ++j) {
+            const int64_t slot = t * a.top_k + min(j0 + j, a.top_k - 1);
+            const int64_t at = a.pos[slot];
+            w[j] = a.weights[slot];
+            h[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (j0 + j >= a.top_k || at < 0 || at >= a.rows) {
+                w[j] = 0.0f;  // nothing: 0 * 0
+            } else if constexpr (VEC) {
+                h[j] = *reinterpret_cast<const f32x4*>(a.h + at * a.n + n0);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n0 + e < a.n) h[j][e] = a.h[at * a.n + n0 + e];
+            }
         }
-    }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + q * kThreads;
-        if (n < a.n) store_y<YT>(a.y, t * a.n + n, s[q]);
+        for (int j = 0; j < S; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(w[j], h[j][e], s[e]);
+    }
+    const int64_t at = t * a.n + n0;
+    if constexpr (VEC) {
+        if constexpr (YT == 0) {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = s;
+        } else {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+                make_uint2(f32_to_bf16(s[0]) | (f32_to_bf16(s[1]) << 16), f32_to_bf16(s[2]) | (f32_to_bf16(s[3]) << 16));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + e < a.n) store_y<YT>(a.y, at + e, s[e]);
     }
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
     CombineParams p;
     p.a = a;
-    p.nblocks = (a.n + 4 * kThreads - 1) / (4 * kThreads);
-    return launch_blocks(a.tokens * p.nblocks, kThreads, [&](uint32_t grid, int64_t block0) {
+    // one wave per workgroup where that leaves CUs without work
+    const int threads = a.tokens * ((a.n + 1023) / 1024) < 1024 ? kWave : kThreads;
+    p.cols = 4 * threads;
+    p.nblocks = (a.n + p.cols - 1) / p.cols;
+    const bool vec = a.n % 4 == 0;
+    return launch_blocks(a.tokens * p.nblocks, threads, [&](uint32_t grid, int64_t block0) {
         p.block0 = block0;
-        if (a.yt == 0) combine_kernel<0><<<grid, kThreads, 0, st>>>(p);
-        else combine_kernel<1><<<grid, kThreads, 0, st>>>(p);
+        if (a.yt == 0) {
+            if (vec) combine_kernel<0, true><<<grid, threads, 0, st>>>(p);
+            else combine_kernel<0, false><<<grid, threads, 0, st>>>(p);
+        } else {
+            if (vec) combine_kernel<1, true><<<grid, threads, 0, st>>>(p);
+            else combine_kernel<1, false><<<grid, threads, 0, st>>>(p);
+        }
     });
 }
 
