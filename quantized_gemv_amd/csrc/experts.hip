@@ -66,21 +66,39 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 // v_mfma_f32_16x16x32_bf16 (or v_mfma_i32_16x16x64_i8) that share the x
 // fragments, and their sums meet in LDS in order.  A unit of 64 k is loaded
 // while the one before it is multiplied, and the first codes are requested
-// before the rows of x are known.  Quarters start at whole 128-byte lines of
-// row-major codes; tiled codes are read as whole blocks, once each:
+// before the rows of x are known.  Codes are read in whole 128-byte lines
+// (row-major: a pair of units at a time; tiled: blocks of 1 KB), once each:
 // non-temporal.
 //
-// HBM bounds it.  Small workgroups with little in registers keep the most of
+// HkTM bounds it.  Small workgroups with little in registers keep the most of
 // them on a CU, so that one's start (tile search, row numbers) and end hide
 // behind the others' loads.  Waves per workgroup x tiles per wave x units per
 // step, us of the four cases with few rows (180, 237, 119 and 94 MB of codes):
 // 4 x 2 x 1: 32.5, 32.8, 24.6, 25.0; 4 x 4 x 2: 34.1, 36.3, 26.1, 25.0;
 // 8 x 4 x 2: 35.7, 45.0, 30.9, 29.2; 2 x 2 x 1: 33.9, 33.0, 25.0, 26.1.
+// Row-major codes, two loads of 16 bytes per lane that read whole 128-byte
+// lines: r1 holds row l % 8, r2 row 8 + l % 8, both chunk l / 8 of the line's
+// eight.  The matrix instructions want row l % 16 and one chunk for all rows:
+// lanes 8 apart exchange halves, after which r1 holds chunk 2 (l / 16) of row
+// l % 16 and r2 the chunk after it.
+__device__ __forceinline__ void line_halves(u32x4& r1, u32x4& r2) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int a = (int)r1[d], b = (int)r2[d];
+        r1[d] = (uint32_t)__builtin_amdgcn_update_dpp(a, b, 0x128, 0xF, 0xC, false);  // row_ror:8 into lanes 8-15
+        r2[d] = (uint32_t)__builtin_amdgcn_update_dpp(b, a, 0x128, 0xF, 0x3, false);  // and into lanes 0-7
+    }
+}
+
 template <int ACT, int YT, bool GLU, bool TILED>
-__global__ __launch_bounds__(kEThreads) void experts_stream_kernel(ExpertParams p) {
+__global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertParams p) {
     constexpr int NT = 2;
     constexpr int OT = GLU ? 1 : NT;      // 16-row output tiles
-    constexpr int XF = ACT == 0 ? 2 : 1;  // x loads per unit
+    constexpr int U = TILED ? 1 : 2;      // units loaded together: row-major lines hold two
+    // sets of registers, D - 1 of them on their way while one is multiplied
+    // (row-major: one set, reloaded after its products, and more waves)
+    constexpr int D = TILED ? 3 : 1;
+    constexpr int XF = ACT == 0 ? 2 : 1;  // x loads per unit and 16 rows
     typedef typename std::conditional<ACT == 0, f32x4, i32x4>::type acc_t;
     __shared__ acc_t part[kEWaves][NT][kWave];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -94,7 +112,7 @@ __global__ __launch_bounds__(kEThreads) void experts_stream_kernel(ExpertParams 
     const int pairs = p.k / (2 * kEUnit);
     const int c0 = 2 * (pairs * wave / kEWaves), c1 = 2 * (pairs * (wave + 1) / kEWaves);
     __amdgpu_buffer_rsrc_t rw[NT];
-    uint32_t woff[NT];
+    uint32_t woff[NT][U];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
         // rows past n: row-major codes repeat the last row; tiled codes are
@@ -102,95 +120,118 @@ __global__ __launch_bounds__(kEThreads) void experts_stream_kernel(ExpertParams 
         const int ot = min(ot0 + q % OT, (p.n - 1) / 16);
         rw[q] = make_rsrc(p.codes[GLU ? q : 0] + (int64_t)t.group * p.expert_bytes + (int64_t)ot * 16 * p.k,
                           (uint32_t)(16 * p.k));
-        woff[q] = TILED ? (uint32_t)(lane * 16) : (uint32_t)(min(i, p.n - 1 - 16 * ot) * p.k + g * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            woff[q][u] = TILED ? (uint32_t)(lane * 16)
+                               : (uint32_t)(min((lane & 7) + 8 * u, p.n - 1 - 16 * ot) * p.k + (lane >> 3) * 16);
     }
-    struct Unit {
-        u32x4 w[NT], x[XF];
+    struct Units {
+        u32x4 w[NT][U], x[U][XF];
     };
-    auto load_w = [&](int c, Unit& s) {
+    auto load_w = [&](int c, Units& s) {
 #pragma unroll
         for (int q = 0; q < NT; ++q)
-            s.w[q] = __builtin_amdgcn_raw_buffer_load_b128(rw[q], woff[q], c * (TILED ? 1024 : 64), TILED ? kCachePolicyNT : 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                s.w[q][u] = __builtin_amdgcn_raw_buffer_load_b128(rw[q], woff[q][u], c * (TILED ? 1024 : 64), kCachePolicyNT);
     };
-    Unit sa, sb;
-    if (c0 < c1) load_w(c0, sa);
+    Units s[D];
+    if (c0 < c1) load_w(c0, s[0]);
     __builtin_amdgcn_sched_barrier(0);
     // this lane's x row (rows past the tile repeat its last)
+    constexpr int kX = ACT == 0 ? 2 : 1;  // bytes of an x value
     const int at = t.row0 + min(i, t.rows - 1);
     const int src = min(max(p.order ? p.order[at] / p.per_row : at, 0), p.x_rows - 1);
-    const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + (int64_t)src * p.k * (ACT == 0 ? 2 : 1) + (ACT == 0 ? 32 : 16) * g;
-    auto load_x = [&](int c, Unit& s) {
+    const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + (int64_t)src * p.k * kX + 16 * U * kX * g;
+    auto load_x = [&](int c, Units& s) {
 #pragma unroll
-        for (int f = 0; f < XF; ++f)
-            s.x[f] = *reinterpret_cast<const u32x4*>(xrow + (int64_t)c * (ACT == 0 ? 128 : 64) + 16 * f);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int f = 0; f < XF; ++f)
+                s.x[u][f] = *reinterpret_cast<const u32x4*>(xrow + (int64_t)c * (64 * kX) + 16 * (u * kX + f));
     };
     acc_t acc[NT];
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[q] = acc_t{0, 0, 0, 0};
-    auto multiply = [&](const Unit& s) {
+    auto multiply = [&](Units& s) {
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
-            if constexpr (ACT == 0) {
-                bf16x8 a0, a1;
-                codes_to_bf16(s.w[q], a0, a1);
-                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, s.x[0]), acc[q], 0, 0, 0);
-                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, s.x[XF - 1]), acc[q], 0, 0, 0);
-            } else {
-                acc[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, s.w[q]),
-                                                               __builtin_bit_cast(i32x4, s.x[0]), acc[q], 0, 0, 0);
+            if constexpr (!TILED) line_halves(s.w[q][0], s.w[q][1]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if constexpr (ACT == 0) {
+                    bf16x8 w0, w1;
+                    codes_to_bf16(s.w[q][u], w0, w1);
+                    acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8, s.x[u][0]), acc[q], 0, 0, 0);
+                    acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8, s.x[u][XF - 1]), acc[q], 0, 0, 0);
+                } else {
+                    acc[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, s.w[q][u]),
+                                                                   __builtin_bit_cast(i32x4, s.x[u][0]), acc[q], 0, 0, 0);
+                }
             }
         }
     };
-    if (c0 < c1) {
-        load_x(c0, sa);
-        // a quarter holds whole pairs of units
-        for (int c = c0; c < c1; c += 2) {
-            load_w(c + 1, sb);
-            load_x(c + 1, sb);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(sa);
-            __builtin_amdgcn_sched_barrier(0);
-            if (c + 2 < c1) {
-                load_w(c + 2, sa);
-                load_x(c + 2, sa);
+    bool more = c0 < c1;
+    if (more) {
+        load_x(c0, s[0]);
+#pragma unroll
+        for (int d = 1; d < D - 1; ++d) {
+            if (c0 + d * U < c1) {
+                load_w(c0 + d * U, s[d]);
+                load_x(c0 + d * U, s[d]);
             }
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(sb);
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // this lane's row scales, on their way while the quarters meet
-    float sw[NT][4];
-    if (wave == 0) {
+    // at the end wave w < OT finishes output tile w: its row scales are
+    // requested now
+    float sw[GLU ? 2 : 1][4];
+    if (wave < OT) {
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
+        for (int q = 0; q < (GLU ? 2 : 1); ++q)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                sw[q][r] = p.scale[GLU ? q : 0][(int64_t)t.group * p.n + min(16 * (ot0 + q % OT) + 4 * g + r, p.n - 1)];
+                sw[q][r] = p.scale[q][(int64_t)t.group * p.n + min(16 * (ot0 + wave) + 4 * g + r, p.n - 1)];
+    }
+    for (int c = c0; more;) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (!more) break;
+            const int next = c + (D - 1) * U;
+            if (D > 1 && next < c1) {
+                load_w(next, s[(d + D - 1) % D]);
+                load_x(next, s[(d + D - 1) % D]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(s[d]);
+            __builtin_amdgcn_sched_barrier(0);
+            c += U;
+            more = c < c1;
+            if (D == 1 && more) {
+                load_w(c, s[0]);
+                load_x(c, s[0]);
+            }
+        }
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q) part[wave][q][lane] = acc[q];
     lds_barrier();
     // lane l holds x row l % 16, matrix rows 4 (l / 16) + r
-    if (wave != 0 || i >= t.rows) return;
+    if (wave >= OT || i >= t.rows) return;
+    acc_t sum[GLU ? 2 : 1];
 #pragma unroll
-    for (int w = 1; w < kEWaves; ++w)
+    for (int q = 0; q < (GLU ? 2 : 1); ++q) {
+        sum[q] = part[0][GLU ? q : wave][lane];
 #pragma unroll
-        for (int q = 0; q < NT; ++q) acc[q] += part[w][q][lane];
+        for (int w = 1; w < kEWaves; ++w) sum[q] += part[w][GLU ? q : wave][lane];
+    }
     const float sx = ACT == 0 ? 1.0f : p.s_x[src];
 #pragma unroll
-    for (int q = 0; q < OT; ++q) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int n = 16 * (ot0 + q) + 4 * g + r;
-            if (n < p.n) {
-                float o = (float)acc[q][r] / (ACT == 0 ? sw[q][r] : sw[q][r] * sx);
-                if constexpr (GLU) {
-                    const float u = (float)acc[1][r] / (ACT == 0 ? sw[1][r] : sw[1][r] * sx);
-                    o = swiglu(o, u);
-                }
-                store_y<YT>(p.y, (int64_t)(t.row0 + i) * p.n + n, o);
-            }
+    for (int r = 0; r < 4; ++r) {
+        const int n = 16 * (ot0 + wave) + 4 * g + r;
+        if (n < p.n) {
+            float o = (float)sum[0][r] / (ACT == 0 ? sw[0][r] : sw[0][r] * sx);
+            if constexpr (GLU) o = swiglu(o, (float)sum[1][r] / (ACT == 0 ? sw[1][r] : sw[1][r] * sx));
+            store_y<YT>(p.y, (int64_t)(t.row0 + i) * p.n + n, o);
         }
     }
 }
@@ -236,7 +277,7 @@ struct TileAcc<1> {
 
 template <int ACT, int YT, bool GLU, bool TILED, int MA>
 __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTile& t, int n0, uint8_t* smem,
-                                             const uint32_t (&xoff)[4]) {
+                                             const uint32_t (&xoff)[kTM / 32]) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5;
@@ -275,7 +316,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
         const int at = min(c, nk - 1) * 128;
         uint8_t* dst = smem + (c % kTStages) * kTStageBytes;
 #pragma unroll
-        for (int l = 0; l < 4; ++l) dma16_buffer(rx, dst + (wave + 4 * l) * 1024, xoff[l], at);
+        for (int l = 0; l < MA; ++l) dma16_buffer(rx, dst + (wave + 4 * l) * 1024, xoff[l], at);
     };
     typename TileAcc<ACT>::type acc[MA][2];
 #pragma unroll
@@ -331,7 +372,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     load_x(2);
     __builtin_amdgcn_sched_barrier(0);
     auto step = [&](int c, const Codes& now, Codes& next) {
-        wait_vmcnt<kLoads + 8>();
+        wait_vmcnt<kLoads + 2 * MA>();
         lds_barrier();  // every wave's share of x stage c is there, and no one reads stage c - 1 any more
         load_codes(min(c + 1, nk - 1), next);
         __builtin_amdgcn_sched_barrier(0);
@@ -413,9 +454,9 @@ __global__ __launch_bounds__(kTThreads, 2) void experts_tile_kernel(ExpertParams
         const int src = p.order ? p.order[i] / p.per_row : i;
         return min(max(src, 0), p.x_rows - 1);
     };
-    uint32_t xsrc[4];
+    uint32_t xsrc[kTM / 32];
 #pragma unroll
-    for (int l = 0; l < 4; ++l) {
+    for (int l = 0; l < kTM / 32; ++l) {
         const int row = (wave + 4 * l) * 8 + (lane >> 3);
         xsrc[l] = (uint32_t)source(row) * (uint32_t)(p.k * (ACT == 0 ? 2 : 1)) + 16 * swz<8>(row, lane & 7);
     }
@@ -446,9 +487,17 @@ static hipError_t run_tile(ExpertParams p, hipStream_t st) {
 
 template <int ACT, int YT, bool GLU>
 static hipError_t run_kind(const ExpertParams& p, hipStream_t st) {
+    // Streams up to nine rows per expert, tiles above.  Measured, us, stream and
+    // tile (swiglu, tiled codes, bf16 x): 64 experts of 1024 x 2048 at 4, 8, 12,
+    // 24 rows each 39 46, 50 54, 62 55, 98 61; 8 of 4096 x 4096: 46 52, 49 52,
+    // 62 54, 99 55.  Where the tiles do not fill the CUs a workgroup's own time
+    // decides, and streams hold out longer: 8 of 512 x 1024 at 16, 48, 96 rows
+    // 8 14, 10 20, 14 22.
+    const int per = GLU ? kTN / 2 : kTN;
+    const bool fills = max_row_tiles(p.rows, p.e, kTM) * ((p.n + per - 1) / per) >= 256;
     // the tile kernel keeps 32-bit offsets into x and a tile's y
     const bool small = (int64_t)p.x_rows * p.k * (ACT == 0 ? 2 : 1) < ((int64_t)1 << 32) && p.n < (1 << 21);
-    if (p.rows <= 16 * (int64_t)p.e || !small)
+    if (p.rows <= (fills ? 9 : 96) * (int64_t)p.e || !small)
         return p.tiled ? run_stream<ACT, YT, GLU, true>(p, st) : run_stream<ACT, YT, GLU, false>(p, st);
     return p.tiled ? run_tile<ACT, YT, GLU, true>(p, st) : run_tile<ACT, YT, GLU, false>(p, st);
 }

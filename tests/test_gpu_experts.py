@@ -129,6 +129,10 @@ SIZES = [  # t, e, top, k, n, spread, drop
     (300, 70, 1, 128, 64, "skew", 0.0),
     (600, 6, 2, 512, 520, "skew", 0.05),
     (1100, 4, 1, 256, 272, "one", 0.0),
+    # enough tiles to fill the card with few rows per expert
+    (80, 64, 8, 256, 1030, "skew", 0.0),
+    (200, 33, 4, 384, 2050, "skew", 0.1),
+    (150, 40, 6, 128, 1537, "even", 0.02),
 ]
 
 
