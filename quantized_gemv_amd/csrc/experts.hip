@@ -70,7 +70,7 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 // (row-major: a pair of units at a time; tiled: blocks of 1 KB), once each:
 // non-temporal.
 //
-// HkTM bounds it.  Small workgroups with little in registers keep the most of
+// HBM bounds it.  Small workgroups with little in registers keep the most of
 // them on a CU, so that one's start (tile search, row numbers) and end hide
 // behind the others' loads.  Waves per workgroup x tiles per wave x units per
 // step, us of the four cases with few rows (180, 237, 119 and 94 MB of codes):
@@ -247,11 +247,11 @@ static hipError_t run_stream(ExpertParams p, hipStream_t st) {
 }
 
 // ------------------------------------------------------------------ tiles
-// Many rows per expert: a 256-thread workgroup computes 128 sorted rows of one
-// expert times 256 matrix rows (GLU: 128 of the gate and the same 128 of the
-// up matrix); each of its four waves all 128 rows times 64 matrix rows, 4 x 2
-// tiles of v_mfma_f32_32x32x16_bf16 (or v_mfma_i32_32x32x32_i8).  Two
-// workgroups run on a CU.
+// Many rows per expert: a 256-thread workgroup computes BM = 128 (or 32)
+// sorted rows of one expert times 256 matrix rows (GLU: 128 of the gate and
+// the same 128 of the up matrix); each of its four waves all BM rows times 64
+// matrix rows, BM / 32 x 2 tiles of v_mfma_f32_32x32x16_bf16 (or
+// v_mfma_i32_32x32x32_i8).  Two workgroups run on a CU (four of 32 rows).
 //   x: gathered by direct global->LDS loads (per-lane row addresses) into a
 //      ring of 4 stages of 128 bytes per row, shared by the four waves;
 //      16-byte chunks permuted by the row (swz), free of bank conflicts.
@@ -262,9 +262,8 @@ static hipError_t run_stream(ExpertParams p, hipStream_t st) {
 // costs what its rows need, to 32.  Tiles go expert by expert, four row tiles
 // by all column tiles at a time, and each XCD takes one contiguous run of
 // that order, so the tiles that run together share codes and rows in its L2.
-constexpr int kTM = 128, kTN = 256, kTThreads = 256, kTStages = 4;
-constexpr int kTStageBytes = kTM * 128;
-constexpr size_t kTLds = (size_t)kTStages * kTStageBytes + kTM * sizeof(float);
+constexpr int kTN = 256, kTThreads = 256, kTStages = 4;
+constexpr size_t tile_lds(int bm) { return (size_t)kTStages * bm * 128 + bm * sizeof(float); }
 
 template <int ACT>
 struct TileAcc {
@@ -275,9 +274,9 @@ struct TileAcc<1> {
     typedef i32x16 type;
 };
 
-template <int ACT, int YT, bool GLU, bool TILED, int MA>
+template <int ACT, int YT, bool GLU, bool TILED, int BM, int MA>
 __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTile& t, int n0, uint8_t* smem,
-                                             const uint32_t (&xoff)[kTM / 32]) {
+                                             const uint32_t (&xoff)[BM / 32]) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5;
@@ -314,7 +313,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     const int nk = p.k / (ACT == 0 ? 64 : 128);
     auto load_x = [&](int c) {
         const int at = min(c, nk - 1) * 128;
-        uint8_t* dst = smem + (c % kTStages) * kTStageBytes;
+        uint8_t* dst = smem + (c % kTStages) * (BM * 128);
 #pragma unroll
         for (int l = 0; l < MA; ++l) dma16_buffer(rx, dst + (wave + 4 * l) * 1024, xoff[l], at);
     };
@@ -328,7 +327,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
 
     const int xrow = (lane & 31) * 128, xswz = (lane >> 1) & 7;  // swz of a row: its chunk ^ xswz
     auto multiply = [&](int c, const Codes& w) {
-        const uint8_t* xs = smem + (c % kTStages) * kTStageBytes + xrow;
+        const uint8_t* xs = smem + (c % kTStages) * (BM * 128) + xrow;
         bf16x8 wb[2][2];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -391,7 +390,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     // lane l holds output column l % 32 of each block, rows 8 (r / 4) + 4 (l / 32) + r % 4;
     // stores past the tile's rows fall outside the buffer's range and are dropped
     constexpr int kY = YT == 0 ? 4 : 2;
-    const float* rsx = reinterpret_cast<const float*>(smem + kTStages * kTStageBytes);
+    const float* rsx = reinterpret_cast<const float*>(smem + kTStages * (BM * 128));
     const __amdgpu_buffer_rsrc_t ry =
         make_rsrc(static_cast<uint8_t*>(p.y) + (int64_t)t.row0 * p.n * kY, (uint32_t)(t.rows * p.n * kY));
     const uint32_t line = (uint32_t)(p.n * kY);
@@ -425,28 +424,28 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     }
 }
 
-template <int ACT, int YT, bool GLU, bool TILED>
-__global__ __launch_bounds__(kTThreads, 2) void experts_tile_kernel(ExpertParams p) {
+template <int ACT, int YT, bool GLU, bool TILED, int BM>
+__global__ __launch_bounds__(kTThreads, BM == 32 ? 4 : 2) void experts_tile_kernel(ExpertParams p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the tile: consecutive workgroups go to different XCDs, each XCD gets a
     // contiguous run of the tiles there are (the grid is sized for the most
     // there can be)
-    const int64_t total = (int64_t)count_row_tiles<kTM>(p.offsets, p.e, p.rows) * p.ntiles;
+    const int64_t total = (int64_t)count_row_tiles<BM>(p.offsets, p.e, p.rows) * p.ntiles;
     const int64_t block = p.block0 + blockIdx.x, per = (total + 7) >> 3;
     const int64_t at = (block & 7) * per + (block >> 3);
     if ((block >> 3) >= per || at >= total) return;
-    RowTile t = find_row_tile<kTM>(p.offsets, p.e, p.rows, (int)(at / p.ntiles));
+    RowTile t = find_row_tile<BM>(p.offsets, p.e, p.rows, (int)(at / p.ntiles));
     if (t.rows <= 0) return;
     const int64_t r = at - (int64_t)t.before * p.ntiles;
-    const int mt = (t.count + kTM - 1) / kTM;
+    const int mt = (t.count + BM - 1) / BM;
     const int st = (int)(r / (4 * (int64_t)p.ntiles));
     const int u = (int)(r - (int64_t)st * 4 * p.ntiles), tall = min(4, mt - 4 * st);
     const int m = 4 * st + u % tall;
     const int n0 = u / tall * (GLU ? kTN / 2 : kTN);
-    t.row0 = t.first + m * kTM;
-    t.rows = min(kTM, t.count - m * kTM);
+    t.row0 = t.first + m * BM;
+    t.rows = min(BM, t.count - m * BM);
 
     // rows past the tile repeat its last row
     auto source = [&](int row) {
@@ -454,52 +453,62 @@ __global__ __launch_bounds__(kTThreads, 2) void experts_tile_kernel(ExpertParams
         const int src = p.order ? p.order[i] / p.per_row : i;
         return min(max(src, 0), p.x_rows - 1);
     };
-    uint32_t xsrc[kTM / 32];
+    uint32_t xsrc[BM / 32];
 #pragma unroll
-    for (int l = 0; l < kTM / 32; ++l) {
+    for (int l = 0; l < BM / 32; ++l) {
         const int row = (wave + 4 * l) * 8 + (lane >> 3);
         xsrc[l] = (uint32_t)source(row) * (uint32_t)(p.k * (ACT == 0 ? 2 : 1)) + 16 * swz<8>(row, lane & 7);
     }
     if constexpr (ACT == 1) {
         // read after the barriers of the k loop
-        if (tid < kTM) reinterpret_cast<float*>(smem + kTStages * kTStageBytes)[tid] = 1.0f / p.s_x[source(tid)];
+        if (tid < BM) reinterpret_cast<float*>(smem + kTStages * (BM * 128))[tid] = 1.0f / p.s_x[source(tid)];
     }
-    if (t.rows > 96) experts_tile<ACT, YT, GLU, TILED, 4>(p, t, n0, smem, xsrc);
-    else if (t.rows > 64) experts_tile<ACT, YT, GLU, TILED, 3>(p, t, n0, smem, xsrc);
-    else if (t.rows > 32) experts_tile<ACT, YT, GLU, TILED, 2>(p, t, n0, smem, xsrc);
-    else experts_tile<ACT, YT, GLU, TILED, 1>(p, t, n0, smem, xsrc);
+    if constexpr (BM == 32) {
+        experts_tile<ACT, YT, GLU, TILED, BM, 1>(p, t, n0, smem, xsrc);
+    } else {
+        if (t.rows > 96) experts_tile<ACT, YT, GLU, TILED, BM, 4>(p, t, n0, smem, xsrc);
+        else if (t.rows > 64) experts_tile<ACT, YT, GLU, TILED, BM, 3>(p, t, n0, smem, xsrc);
+        else if (t.rows > 32) experts_tile<ACT, YT, GLU, TILED, BM, 2>(p, t, n0, smem, xsrc);
+        else experts_tile<ACT, YT, GLU, TILED, BM, 1>(p, t, n0, smem, xsrc);
+    }
 }
 
-template <int ACT, int YT, bool GLU, bool TILED>
+template <int ACT, int YT, bool GLU, bool TILED, int BM>
 static hipError_t run_tile(ExpertParams p, hipStream_t st) {
-    auto kern = experts_tile_kernel<ACT, YT, GLU, TILED>;
+    auto kern = experts_tile_kernel<ACT, YT, GLU, TILED, BM>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kTLds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)tile_lds(BM));
     if (e != hipSuccess) return e;
     const int per = GLU ? kTN / 2 : kTN;
     p.ntiles = (p.n + per - 1) / per;
-    const int64_t blocks = (max_row_tiles(p.rows, p.e, kTM) * p.ntiles + 7) / 8 * 8;
+    const int64_t blocks = (max_row_tiles(p.rows, p.e, BM) * p.ntiles + 7) / 8 * 8;
     return launch_blocks(blocks, kTThreads, [&](uint32_t grid, int64_t block0) {
         p.block0 = block0;
-        kern<<<grid, kTThreads, kTLds, st>>>(p);
+        kern<<<grid, kTThreads, tile_lds(BM), st>>>(p);
     });
 }
 
 template <int ACT, int YT, bool GLU>
 static hipError_t run_kind(const ExpertParams& p, hipStream_t st) {
     // Streams up to nine rows per expert, tiles above.  Measured, us, stream and
-    // tile (swiglu, tiled codes, bf16 x): 64 experts of 1024 x 2048 at 4, 8, 12,
-    // 24 rows each 39 46, 50 54, 62 55, 98 61; 8 of 4096 x 4096: 46 52, 49 52,
-    // 62 54, 99 55.  Where the tiles do not fill the CUs a workgroup's own time
-    // decides, and streams hold out longer: 8 of 512 x 1024 at 16, 48, 96 rows
-    // 8 14, 10 20, 14 22.
-    const int per = GLU ? kTN / 2 : kTN;
-    const bool fills = max_row_tiles(p.rows, p.e, kTM) * ((p.n + per - 1) / per) >= 256;
+    // 128-row tiles (swiglu, tiled codes, bf16 x): 64 experts of 1024 x 2048 at
+    // 4, 8, 12, 24 rows each 39 46, 50 54, 62 55, 98 61; 8 of 4096 x 4096: 46 52,
+    // 49 52, 62 54, 99 55.  Where 128-row tiles do not fill the CUs, a
+    // workgroup's own time decides: 32-row tiles then, or streams while all of
+    // them together read few matrix rows.  Stream, 32-row, 128-row tiles
+    // (products): 5 of 440 x 2176 at 64, 256, 1024 rows 13 17 30, 22 18 34, 71 27
+    // 36; 16 of 1024 x 2048 at 16, 32, 128 rows 14 17 19, 20 17 25, 53 25 34; at
+    // 256 tiles of 128 rows and above the two tiles are even (32 of 704 x 1024,
+    // 256 rows: 26 23), and with more of them 128 rows win.
+    constexpr int kPer = GLU ? kTN / 2 : kTN;
+    const bool fills = max_row_tiles(p.rows, p.e, 128) * ((p.n + kPer - 1) / kPer) >= 256;
+    const int64_t streamed = max_row_tiles(p.rows, p.e, 16) * p.n * (GLU ? 2 : 1);
     // the tile kernel keeps 32-bit offsets into x and a tile's y
     const bool small = (int64_t)p.x_rows * p.k * (ACT == 0 ? 2 : 1) < ((int64_t)1 << 32) && p.n < (1 << 21);
-    if (p.rows <= (fills ? 9 : 96) * (int64_t)p.e || !small)
+    if (p.rows <= 9 * (int64_t)p.e || (!fills && streamed < 28000) || !small)
         return p.tiled ? run_stream<ACT, YT, GLU, true>(p, st) : run_stream<ACT, YT, GLU, false>(p, st);
-    return p.tiled ? run_tile<ACT, YT, GLU, true>(p, st) : run_tile<ACT, YT, GLU, false>(p, st);
+    if (!fills) return p.tiled ? run_tile<ACT, YT, GLU, true, 32>(p, st) : run_tile<ACT, YT, GLU, false, 32>(p, st);
+    return p.tiled ? run_tile<ACT, YT, GLU, true, 128>(p, st) : run_tile<ACT, YT, GLU, false, 128>(p, st);
 }
 template <int ACT, int YT>
 static hipError_t run_glu(const ExpertParams& p, bool glu, hipStream_t st) {

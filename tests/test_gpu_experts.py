@@ -133,6 +133,9 @@ SIZES = [  # t, e, top, k, n, spread, drop
     (80, 64, 8, 256, 1030, "skew", 0.0),
     (200, 33, 4, 384, 2050, "skew", 0.1),
     (150, 40, 6, 128, 1537, "even", 0.02),
+    # many rows, too few 128-row tiles to fill the card
+    (500, 5, 3, 640, 440, "skew", 0.0),
+    (333, 30, 5, 256, 391, "skew", 0.1),
 ]
 
 
