@@ -259,10 +259,22 @@ static hipError_t run_stream(ExpertParams p, hipStream_t st) {
 //      registers, 16 bytes per lane, one stage ahead, and are widened to bf16
 //      there (exact).
 // Waves multiply only the 32-row blocks that hold rows: a group's last tile
-// costs what its rows need, to 32.  Tiles go expert by expert, four row tiles
+// costs what its rows need, to 32.  Tiles go expert by expert, kTall row tiles
 // by all column tiles at a time, and each XCD takes one contiguous run of
 // that order, so the tiles that run together share codes and rows in its L2.
+//
+// 2048 tokens, 8 experts of 2 x 11008 x 4096, bf16 x: 704 us, 1.05 PFLOP/s.
+// What holds it, from runs with parts taken out: the matrix instructions alone
+// take 453 us (the clock falls to 1.8 GHz under them), without the LDS reads
+// 597, without the widening 651, with neither x nor codes loaded 466: the loads
+// cost most.  They are not late (codes two stages ahead: no change) and not
+// from far (the L2s miss 1 GB of 6.5 GB asked), so it is the L1s' and L2s' rate.
+// Tried and slower: 256 rows by eight waves, one workgroup per CU (796: fewer
+// bytes, but no second workgroup to cover the barrier), one, two, four row
+// tiles at a time (808, 750, 726 against 715 with eight).  Loads between the
+// products instead of before them and a raised wave priority: 3.5%.
 constexpr int kTN = 256, kTThreads = 256, kTStages = 4;
+constexpr int kTall = 8;  // row tiles that go through the column tiles together
 constexpr size_t tile_lds(int bm) { return (size_t)kTStages * bm * 128 + bm * sizeof(float); }
 
 template <int ACT>
@@ -302,20 +314,18 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     struct Codes {
         u32x4 v[2][kPieces];
     };
-    auto load_codes = [&](int c, Codes& w) {
+    auto load_codes = [&](int c, int b, Codes& w) {
         const int at = c * (kPieces / 2 * kUnit);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int q = 0; q < kPieces; ++q)
-                w.v[b][q] = __builtin_amdgcn_raw_buffer_load_b128(rw[b], woff[b] + (q >> 1) * kUnit + (q & 1) * kPair, at, 0);
+        for (int q = 0; q < kPieces; ++q)
+            w.v[b][q] = __builtin_amdgcn_raw_buffer_load_b128(rw[b], woff[b] + (q >> 1) * kUnit + (q & 1) * kPair, at, 0);
     };
     const int nk = p.k / (ACT == 0 ? 64 : 128);
-    auto load_x = [&](int c) {
+    auto load_x = [&](int c, int first, int step) {
         const int at = min(c, nk - 1) * 128;
         uint8_t* dst = smem + (c % kTStages) * (BM * 128);
 #pragma unroll
-        for (int l = 0; l < MA; ++l) dma16_buffer(rx, dst + (wave + 4 * l) * 1024, xoff[l], at);
+        for (int l = first; l < MA; l += step) dma16_buffer(rx, dst + (wave + 4 * l) * 1024, xoff[l], at);
     };
     typename TileAcc<ACT>::type acc[MA][2];
 #pragma unroll
@@ -326,11 +336,12 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0;
 
     const int xrow = (lane & 31) * 128, xswz = (lane >> 1) & 7;  // swz of a row: its chunk ^ xswz
-    auto multiply = [&](int c, const Codes& w) {
+    auto multiply = [&](int c, const Codes& w, const auto& between) {
         const uint8_t* xs = smem + (c % kTStages) * (BM * 128) + xrow;
         bf16x8 wb[2][2];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            between(q);
             const int chunk = ACT == 0 ? 4 * (q >> 1) + 2 * h + (q & 1) : 2 * q + h;
             u32x4 xf[MA];
 #pragma unroll
@@ -363,21 +374,31 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     // this order: at its start at most x of c + 1, codes of c and x of c + 2
     // may be outstanding, which leaves x of c landed.
     Codes wa, wb;
-    load_x(0);
-    load_x(1);
+    load_x(0, 0, 1);
+    load_x(1, 0, 1);
     __builtin_amdgcn_sched_barrier(0);
-    load_codes(0, wa);
+    load_codes(0, 0, wa);
+    load_codes(0, 1, wa);
     __builtin_amdgcn_sched_barrier(0);
-    load_x(2);
+    load_x(2, 0, 1);
     __builtin_amdgcn_sched_barrier(0);
     auto step = [&](int c, const Codes& now, Codes& next) {
         wait_vmcnt<kLoads + 2 * MA>();
         lds_barrier();  // every wave's share of x stage c is there, and no one reads stage c - 1 any more
-        load_codes(min(c + 1, nk - 1), next);
-        __builtin_amdgcn_sched_barrier(0);
-        load_x(c + 3);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(c, now);
+        // the loads go between the products, so that no run of them holds the
+        // matrix unit up: codes in front of quarters 0 and 1, x of 2 and 3
+        const int wat = min(c + 1, nk - 1), xat = c + 3;
+        __builtin_amdgcn_s_setprio(1);
+        multiply(c, now, [&](int q) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (q < 2) {
+                load_codes(wat, q, next);
+            } else {
+                load_x(xat, q & 1, 2);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
     for (int c = 0; c + 1 < nk; c += 2) {
@@ -440,9 +461,9 @@ __global__ __launch_bounds__(kTThreads, BM == 32 ? 4 : 2) void experts_tile_kern
     if (t.rows <= 0) return;
     const int64_t r = at - (int64_t)t.before * p.ntiles;
     const int mt = (t.count + BM - 1) / BM;
-    const int st = (int)(r / (4 * (int64_t)p.ntiles));
-    const int u = (int)(r - (int64_t)st * 4 * p.ntiles), tall = min(4, mt - 4 * st);
-    const int m = 4 * st + u % tall;
+    const int st = (int)(r / (kTall * (int64_t)p.ntiles));
+    const int u = (int)(r - (int64_t)st * kTall * p.ntiles), tall = min(kTall, mt - kTall * st);
+    const int m = kTall * st + u % tall;
     const int n0 = u / tall * (GLU ? kTN / 2 : kTN);
     t.row0 = t.first + m * BM;
     t.rows = min(BM, t.count - m * BM);
