@@ -813,14 +813,15 @@ def _plan_buffers(x: torch.Tensor, rows: int, groups: int, per_row: int, out: Op
 
 def group_rows(ids: torch.Tensor, groups: int, out: Optional[RowGroups] = None,
                ws: Optional[torch.Tensor] = None) -> RowGroups:
-    """Rows sorted by id (qg_group_rows): ids int32 [rows] (ids outside
-    [0, groups) have no group) -> RowGroups.  A serving step makes one plan of
-    its rows' adapters and uses it for every layer and projection."""
+    """Rows sorted by id (qg_group_rows): ids int32 [rows], or [tokens][top_k]
+    as another router gives them (per_row = top_k); ids outside [0, groups)
+    have no group. -> RowGroups.  A serving step makes one plan of its rows'
+    adapters and uses it for every layer and projection."""
     _dev(ids, "ids", torch.int32)
-    if ids.dim() != 1:
-        raise ValueError("ids must be [rows]")
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids must be [rows] or [tokens][top_k]")
     rows = ids.numel()
-    out = _plan_buffers(ids, rows, groups, 1, out)
+    out = _plan_buffers(ids, rows, groups, 1 if ids.dim() == 1 else ids.shape[1], out)
     ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(rows, groups)), ids)
     _call("qg_group_rows", ids, _ptr(ids), rows, groups, _ptr(out.offsets), _ptr(out.order), _ptr(out.pos), _ptr(ws), nws)
     return out

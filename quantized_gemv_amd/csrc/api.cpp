@@ -824,7 +824,9 @@ size_t qg_lora_workspace_bytes(const qg_lora* m, int32_t count, int64_t rows, in
     if (rank == 0 || rows < 1 || rows > QG_MAX_PLAN_ROWS || groups < 1 || groups > QG_MAX_ROW_GROUPS || k < 128 ||
         k % 128 != 0 || k > QG_BATCH_MAX_K)
         return 0;
-    return qg::lora_workspace(rows, groups, k, count, rank);
+    int32_t rmax = 0;
+    for (int32_t j = 0; j < count; ++j) rmax = m[j].r > rmax ? m[j].r : rmax;
+    return qg::lora_workspace(rows, groups, k, count, rmax, rank);
 }
 
 qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* groups, const void* x, int64_t x_rows,

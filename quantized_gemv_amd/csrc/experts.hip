@@ -229,9 +229,14 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
     for (int r = 0; r < 4; ++r) {
         const int n = 16 * (ot0 + wave) + 4 * g + r;
         if (n < p.n) {
-            float o = (float)sum[0][r] / (ACT == 0 ? sw[0][r] : sw[0][r] * sx);
-            if constexpr (GLU) o = swiglu(o, (float)sum[1][r] / (ACT == 0 ? sw[1][r] : sw[1][r] * sx));
-            store_y<YT>(p.y, (int64_t)(t.row0 + i) * p.n + n, o);
+            float o[GLU ? 2 : 1];
+#pragma unroll
+            for (int q = 0; q < (GLU ? 2 : 1); ++q) {
+                o[q] = (float)sum[q][r] / sw[q][r];
+                if constexpr (ACT == 1) o[q] /= sx;  // one after the other: the scales' product may overflow
+            }
+            if constexpr (GLU) o[0] = swiglu(o[0], o[1]);
+            store_y<YT>(p.y, (int64_t)(t.row0 + i) * p.n + n, o[0]);
         }
     }
 }

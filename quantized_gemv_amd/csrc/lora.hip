@@ -34,85 +34,89 @@ struct LoraParams {
     const int32_t* order;
     float* ws;
     int32_t count, groups, rows, x_rows, k, parts;
+    int32_t rgroups;               // shrink: rank groups (the largest rank's)
     int32_t strips, strip_blocks;  // expand: strips of columns (the widest matrix's), blocks per strip
     int64_t block0;
 };
 
 // ------------------------------------------------------------------ shrink
-// Eight waves; RT 16-row tiles of A (rank <= 16 RT).  A wave takes up to four
-// of them and a share of the part's k: waves that share tiles split k, and
-// their sums meet in LDS.
+// Eight waves share the part's k of up to four 16-row tiles of A (ranks 64 rg
+// .. + 63, RT tiles); their sums meet in LDS.
 constexpr int kSWaves = 8;
 constexpr int kSThreads = kSWaves * kWave;
+constexpr int kSRanks = 64;  // ranks of a workgroup
 
 template <int RT>
-__device__ __forceinline__ void shrink_tile(const LoraParams& p, const LoraMatP& m, const RowTile& t, int kpart,
+__device__ __forceinline__ void shrink_tile(const LoraParams& p, const LoraMatP& m, const RowTile& t, int kpart, int rg,
                                             f32x4 (&red)[kSWaves][4][kWave]) {
-    constexpr int RTW = RT < 4 ? RT : 4, RG = RT / RTW, KW = kSWaves / RG;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int rg = wave / KW, share = kpart * KW + wave % KW, shares = p.parts * KW;
+    const int share = kpart * kSWaves + wave, shares = p.parts * kSWaves;
     const int units = p.k / 32;
     const int c0 = (int)((int64_t)units * share / shares), c1 = (int)((int64_t)units * (share + 1) / shares);
     const int src = min(max(p.order[t.row0 + min(i, t.rows - 1)], 0), p.x_rows - 1);
     const uint16_t* x = p.x + (int64_t)src * p.k + 8 * g;
-    const uint16_t* a[RTW];
-    f32x4 acc[RTW];
+    const uint16_t* a[RT];
+    f32x4 acc[RT];
 #pragma unroll
-    for (int q = 0; q < RTW; ++q) {
-        a[q] = m.a + ((int64_t)t.group * m.r + min(16 * (rg * RTW + q) + i, m.r - 1)) * p.k + 8 * g;
+    for (int q = 0; q < RT; ++q) {
+        a[q] = m.a + ((int64_t)t.group * m.r + min(kSRanks * rg + 16 * q + i, m.r - 1)) * p.k + 8 * g;
         acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     // the loads of several steps are requested together
     auto batch = [&](int c, auto steps) {
         constexpr int U = decltype(steps)::value;
-        u32x4 xf[U], af[U][RTW];
+        u32x4 xf[U], af[U][RT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             xf[u] = *reinterpret_cast<const u32x4*>(x + (c + u) * 32);
 #pragma unroll
-            for (int q = 0; q < RTW; ++q) af[u][q] = *reinterpret_cast<const u32x4*>(a[q] + (c + u) * 32);
+            for (int q = 0; q < RT; ++q) af[u][q] = *reinterpret_cast<const u32x4*>(a[q] + (c + u) * 32);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int q = 0; q < RTW; ++q)
+            for (int q = 0; q < RT; ++q)
                 acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lbf16x8, af[u][q]),
                                                                  __builtin_bit_cast(lbf16x8, xf[u]), acc[q], 0, 0, 0);
     };
-    constexpr int U = RTW == 4 ? 4 : 8;
+    constexpr int U = RT == 4 ? 4 : 8;
     int c = c0;
     for (; c + U <= c1; c += U) batch(c, std::integral_constant<int, U>());
     for (; c + 2 <= c1; c += 2) batch(c, std::integral_constant<int, 2>());
     if (c < c1) batch(c, std::integral_constant<int, 1>());
 #pragma unroll
-    for (int q = 0; q < RTW; ++q) red[wave][q][lane] = acc[q];
+    for (int q = 0; q < RT; ++q) red[wave][q][lane] = acc[q];
     lds_barrier();
     const int rpad = (m.r + 15) / 16 * 16;
-    for (int q = wave; q < rpad / 16; q += kSWaves) {
-        f32x4 s = red[q / RTW * KW][q % RTW][lane];
+    if (wave < RT && kSRanks * rg + 16 * wave < rpad) {
+        f32x4 s = red[0][wave][lane];
 #pragma unroll
-        for (int w = 1; w < KW; ++w) s += red[q / RTW * KW + w][q % RTW][lane];
-        // lane l: sorted row l % 16, ranks 16 q + 4 (l / 16) + r
+        for (int w = 1; w < kSWaves; ++w) s += red[w][wave][lane];
+        // lane l: sorted row l % 16, ranks 64 rg + 16 wave + 4 (l / 16) + r
         if (i < t.rows)
-            *reinterpret_cast<f32x4*>(p.ws + m.ws_at + ((int64_t)kpart * p.rows + t.row0 + i) * rpad + 16 * q + 4 * g) = s;
+            *reinterpret_cast<f32x4*>(p.ws + m.ws_at + ((int64_t)kpart * p.rows + t.row0 + i) * rpad + kSRanks * rg + 16 * wave + 4 * g) = s;
     }
 }
 
 __global__ __launch_bounds__(kSThreads) void lora_shrink_kernel(LoraParams p) {
     __shared__ f32x4 red[kSWaves][4][kWave];
-    const int64_t block = p.block0 + blockIdx.x;
-    const int mi = (int)(block % p.count), kpart = (int)(block / p.count % p.parts);
-    const RowTile t = find_row_tile<16>(p.offsets, p.groups, p.rows, (int)(block / p.count / p.parts));
-    if (t.rows <= 0) return;
+    int64_t block = p.block0 + blockIdx.x;
+    const int mi = (int)(block % p.count);
+    block /= p.count;
+    const int rg = (int)(block % p.rgroups);
+    block /= p.rgroups;
     const LoraMatP& m = p.m[mi];
-    if (m.r <= 16) shrink_tile<1>(p, m, t, kpart, red);
-    else if (m.r <= 32) shrink_tile<2>(p, m, t, kpart, red);
-    else if (m.r <= 64) shrink_tile<4>(p, m, t, kpart, red);
-    else if (m.r <= 128) shrink_tile<8>(p, m, t, kpart, red);
-    else shrink_tile<16>(p, m, t, kpart, red);
+    const int ranks = m.r - kSRanks * rg;
+    if (ranks <= 0) return;
+    const int kpart = (int)(block % p.parts);
+    const RowTile t = find_row_tile<16>(p.offsets, p.groups, p.rows, (int)(block / p.parts));
+    if (t.rows <= 0) return;
+    if (ranks <= 16) shrink_tile<1>(p, m, t, kpart, rg, red);
+    else if (ranks <= 32) shrink_tile<2>(p, m, t, kpart, rg, red);
+    else shrink_tile<4>(p, m, t, kpart, rg, red);
 }
 
 // ------------------------------------------------------------------ expand
@@ -328,8 +332,8 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
 }
 
 // Parts of k of the shrink: enough workgroups to fill the CUs.
-static int lora_parts(int64_t rows, int64_t groups, int64_t k, int count) {
-    const int64_t blocks = max_row_tiles(rows, groups, 16) * count;
+static int lora_parts(int64_t rows, int64_t groups, int64_t k, int count, int rmax) {
+    const int64_t blocks = max_row_tiles(rows, groups, 16) * count * ((rmax + kSRanks - 1) / kSRanks);
     int64_t parts = (256 + blocks - 1) / blocks;
     const int64_t most = k / 32 / kSWaves;  // a matrix instruction per wave at least
     if (parts > most) parts = most;
@@ -337,8 +341,8 @@ static int lora_parts(int64_t rows, int64_t groups, int64_t k, int count) {
     return (int)(parts < 1 ? 1 : parts);
 }
 
-size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int count, int64_t padded_rank) {
-    return (size_t)lora_parts(rows, groups, k, count) * (size_t)rows * (size_t)padded_rank * sizeof(float);
+size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int count, int rmax, int64_t padded_rank) {
+    return (size_t)lora_parts(rows, groups, k, count, rmax) * (size_t)rows * (size_t)padded_rank * sizeof(float);
 }
 
 template <int YT, int MT, int KC, int CT>
@@ -377,17 +381,19 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t st) {
     p.rows = (int32_t)a.rows;
     p.x_rows = (int32_t)a.x_rows;
     p.k = (int32_t)a.k;
-    p.parts = lora_parts(a.rows, a.groups, a.k, a.count);
     int64_t at = 0, widest = 0;
     int rmax = 0;
+    for (int j = 0; j < a.count; ++j)
+        if (a.m[j].r > rmax) rmax = a.m[j].r;
+    p.parts = lora_parts(a.rows, a.groups, a.k, a.count, rmax);
+    p.rgroups = (rmax + kSRanks - 1) / kSRanks;
     for (int j = 0; j < a.count; ++j) {
         const LoraMat& m = a.m[j];
         p.m[j] = {m.a, m.b, m.scale, m.y, (int32_t)m.n, m.r, at};
         at += (int64_t)p.parts * a.rows * ((m.r + 15) / 16 * 16);
         if (m.n > widest) widest = m.n;
-        if (m.r > rmax) rmax = m.r;
     }
-    const hipError_t e = launch_blocks(max_row_tiles(a.rows, a.groups, 16) * p.parts * p.count, kSThreads,
+    const hipError_t e = launch_blocks(max_row_tiles(a.rows, a.groups, 16) * p.parts * p.rgroups * p.count, kSThreads,
                                        [&](uint32_t grid, int64_t block0) {
                                            p.block0 = block0;
                                            lora_shrink_kernel<<<grid, kSThreads, 0, st>>>(p);

@@ -213,7 +213,8 @@ struct LoraArgs {
     int64_t rows;
     void* ws;
 };
-size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int count, int64_t padded_rank);
+size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int count, int rmax,
+                      int64_t padded_rank);
 hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
 
 int device_cu_count();

@@ -74,6 +74,16 @@ def test_group_rows_one_group_holds_all_and_none(qg):
         check_plan(qg.group_rows(dev(ids), 7), *plan_fast(ids, 7))
 
 
+def test_group_rows_of_another_router(qg):
+    note("group_rows of ids [tokens][top_k]")
+    ids = synth.rng(6).integers(-1, 9, (50, 3)).astype(np.int32)
+    plan = qg.group_rows(dev(ids), 9)
+    check_plan(plan, *plan_fast(ids.reshape(-1), 9))
+    assert plan.per_row == 3
+    with pytest.raises(ValueError):
+        qg.group_rows(dev(ids.reshape(5, 10, 3)), 9)
+
+
 def test_group_rows_reused_buffers(qg):
     note("group_rows into given buffers and workspace, a smaller input after a larger one")
     g = synth.rng(5)
