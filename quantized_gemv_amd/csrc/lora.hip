@@ -365,8 +365,8 @@ static hipError_t launch_expand(LoraParams& p, int rmax, int64_t widest, hipStre
     // 32 rows per workgroup where the groups have that many
     const bool tall = p.rows >= 32 * (int64_t)p.groups;
     if (rmax <= 32) return tall ? run_expand<YT, 2, 1, 2>(p, widest, st) : run_expand<YT, 1, 1, 4>(p, widest, st);
-    if (rmax <= 64) return tall ? run_expand<YT, 2, 2, 2>(p, widest, st) : run_expand<YT, 1, 2, 4>(p, widest, st);
-    if (rmax <= 128) return tall ? run_expand<YT, 2, 4, 1>(p, widest, st) : run_expand<YT, 1, 4, 2>(p, widest, st);
+    if (rmax <= 64) return tall ? run_expand<YT, 2, 2, 2>(p, widest, st) : run_expand<YT, 1, 2, 2>(p, widest, st);
+    if (rmax <= 128) return tall ? run_expand<YT, 2, 4, 2>(p, widest, st) : run_expand<YT, 1, 4, 2>(p, widest, st);
     return tall ? run_expand<YT, 2, 8, 1>(p, widest, st) : run_expand<YT, 1, 8, 1>(p, widest, st);
 }
 
