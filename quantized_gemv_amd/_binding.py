@@ -762,11 +762,11 @@ def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor):
     return ws, ws.numel()
 
 
-@dataclass
+@dataclass(frozen=True)
 class RowGroups:
     """A row plan (qg_group_rows): the rows sorted by group. offsets
     [groups + 1], order and pos [rows], int32 on the device; per_row plan rows
-    read one row of x (a router's top_k)."""
+    read one row of x (a router's top_k).  Checked once, when it is made."""
     offsets: torch.Tensor
     order: torch.Tensor
     pos: torch.Tensor
@@ -778,26 +778,33 @@ class RowGroups:
         _same_device(self.offsets, self.order, self.pos)
         if self.order.numel() != self.pos.numel():
             raise ValueError("order and pos differ in length")
-
-    @property
-    def groups(self) -> int:
-        return self.offsets.numel() - 1
-
-    @property
-    def rows(self) -> int:
-        return self.order.numel()
+        put = object.__setattr__
+        put(self, "groups", self.offsets.numel() - 1)
+        put(self, "rows", self.order.numel())
+        put(self, "ptrs", (self.offsets.data_ptr(), self.order.data_ptr(), self.pos.data_ptr()))
+        put(self, "_c", tuple(CRowGroups(self.ptrs[0], order, self.rows, self.groups, self.per_row)
+                              for order in (None, self.ptrs[1])))
 
     def c_struct(self, gather: bool = True) -> CRowGroups:
-        return CRowGroups(self.offsets.data_ptr(), self.order.data_ptr() if gather else None, self.rows, self.groups,
-                          self.per_row)
+        return self._c[1 if gather else 0]
 
 
-@dataclass
+@dataclass(frozen=True)
 class Routing:
-    """What moe_route returns: ids and weights [tokens][top_k] and the plan."""
+    """What moe_route returns: ids and weights [tokens][top_k] and the plan.
+    Checked once, when it is made."""
     ids: torch.Tensor
     weights: torch.Tensor
     groups: RowGroups
+
+    def __post_init__(self):
+        _dev(self.ids, "ids", torch.int32)
+        _dev(self.weights, "weights", torch.float32)
+        _same_device(self.ids, self.weights, self.groups.offsets)
+        if self.ids.dim() != 2 or self.weights.shape != self.ids.shape or self.ids.numel() != self.groups.rows \
+                or self.ids.shape[1] != self.groups.per_row:
+            raise ValueError("ids and weights must be [tokens][top_k], one per row of the plan")
+        object.__setattr__(self, "ptrs", (self.ids.data_ptr(), self.weights.data_ptr()) + self.groups.ptrs)
 
 
 def _plan_buffers(x: torch.Tensor, rows: int, groups: int, per_row: int, out: Optional[RowGroups]) -> RowGroups:
@@ -823,7 +830,7 @@ def group_rows(ids: torch.Tensor, groups: int, out: Optional[RowGroups] = None,
     rows = ids.numel()
     out = _plan_buffers(ids, rows, groups, 1 if ids.dim() == 1 else ids.shape[1], out)
     ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(rows, groups)), ids)
-    _call("qg_group_rows", ids, _ptr(ids), rows, groups, _ptr(out.offsets), _ptr(out.order), _ptr(out.pos), _ptr(ws), nws)
+    _call("qg_group_rows", ids, _ptr(ids), rows, groups, *out.ptrs, _ptr(ws), nws)
     return out
 
 
@@ -835,16 +842,19 @@ def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, out: Option
     if logits.dim() != 2:
         raise ValueError("logits must be [tokens][experts]")
     t, e = logits.shape
-    ids = _shaped(None if out is None else out.ids, "out.ids", (t, top_k), torch.int32, logits)
-    weights = _shaped(None if out is None else out.weights, "out.weights", (t, top_k), torch.float32, logits)
-    plan = _plan_buffers(logits, t * top_k, e, top_k, None if out is None else out.groups)
+    if out is None:
+        out = Routing(torch.empty((t, top_k), dtype=torch.int32, device=logits.device),
+                      torch.empty((t, top_k), dtype=torch.float32, device=logits.device),
+                      _plan_buffers(logits, t * top_k, e, top_k, None))
+    else:
+        _plan_buffers(logits, t * top_k, e, top_k, out.groups)
     ws, nws = _workspace(ws, int(lib().qg_group_rows_workspace_bytes(t * top_k, e)), logits)
-    _call("qg_moe_route", logits, _ptr(logits), _xt(logits), t, e, top_k, 1 if renorm else 0, _ptr(ids), _ptr(weights),
-          _ptr(plan.offsets), _ptr(plan.order), _ptr(plan.pos), _ptr(ws), nws)
-    return Routing(ids, weights, plan) if out is None else out
+    _call("qg_moe_route", logits, logits.data_ptr(), _xt(logits), t, e, top_k, 1 if renorm else 0, *out.ptrs, _ptr(ws),
+          nws)
+    return out
 
 
-@dataclass
+@dataclass(frozen=True)
 class QExperts:
     """The experts' int8 matrices (qg_experts): codes [e][n][k] (QG_WFMT_INT8)
     or each expert's 16-row tiles (QG_WFMT_INT8_T16, tiled16_experts), scale
@@ -863,7 +873,8 @@ class QExperts:
         per = (self.n + 15) // 16 * 16 if self.fmt == QG_WFMT_INT8_T16 else self.n
         if self.codes.numel() != self.e * per * self.k or self.scale.numel() != self.e * self.n:
             raise ValueError("codes or scale do not hold %d experts of [%d][%d]" % (self.e, self.n, self.k))
-        self._c = CExperts(self.fmt, 0, self.e, self.n, self.k, self.codes.data_ptr(), self.scale.data_ptr())
+        object.__setattr__(self, "_c", CExperts(self.fmt, 0, self.e, self.n, self.k, self.codes.data_ptr(),
+                                                   self.scale.data_ptr()))
 
     def c_struct(self) -> CExperts:
         return self._c
