@@ -841,7 +841,7 @@ qg_status qg_qgemm_experts_combine(const qg_experts* w, const qg_row_groups* gro
  *     [groups][n][r], scale fp32 [groups] or NULL (1), y [x_rows][n] of type yt.
  * x : bf16 [x_rows][k].
  * r % 8 == 0, 8 <= r <= QG_LORA_MAX_R (each matrix its own); k % 128 == 0,
- * 128 <= k <= QG_BATCH_MAX_K; 1 <= n < 2^30; rows <= x_rows < 2^31;
+ * 128 <= k <= QG_BATCH_MAX_K; 4 <= n < 2^30; rows <= x_rows < 2^31;
  * groups <= QG_MAX_ROW_GROUPS; x_rows * k, x_rows * n, groups * n * r and
  * groups * r * k <= 2^40.  a, b, x, y 16-B aligned.
  * ws: qg_lora_workspace_bytes(...) bytes for the same m (its r), count,

@@ -846,7 +846,7 @@ qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* grou
         const qg_lora& mj = m[j];
         if (!mj.a || !mj.b || !mj.y) return QG_ERR_NULLPTR;
         if (mj.r < 8 || mj.r > QG_LORA_MAX_R || mj.r % 8 != 0) return QG_ERR_SHAPE;
-        if (mj.n < 1 || mj.n >= ((int64_t)1 << 30) || !fits(x_rows, mj.n) || !fits(mj.n * groups->groups, mj.r) ||
+        if (mj.n < 4 || mj.n >= ((int64_t)1 << 30) || !fits(x_rows, mj.n) || !fits(mj.n * groups->groups, mj.r) ||
             !fits((int64_t)mj.r * groups->groups, k))
             return QG_ERR_SHAPE;
         if (!aligned16(mj.a) || !aligned16(mj.b) || !aligned16(mj.y) || !aligned_to(mj.scale, 4)) return QG_ERR_ALIGN;

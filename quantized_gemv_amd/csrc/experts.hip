@@ -574,7 +574,11 @@ struct CombineParams {
     int64_t nblocks, block0;
     int32_t cols;  // columns of a workgroup
 };
-template <int YT, bool VEC>
+// four columns, aligned to their elements only (rows of any length)
+typedef float c4f __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t c4h __attribute__((ext_vector_type(2), aligned(2)));
+
+template <int YT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
     constexpr int S = 8;
     const CombineArgs& a = p.a;
@@ -582,6 +586,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
     const int64_t t = block / p.nblocks;
     const int64_t n0 = (block % p.nblocks) * p.cols + 4 * (int)threadIdx.x;
     if (n0 >= a.n) return;
+    const bool whole = n0 + 4 <= a.n;  // else the piece that the row ends in
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < a.top_k; j0 += S) {
         f32x4 h[S];
@@ -594,11 +599,11 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
             h[j] = f32x4{0.f, 0.f, 0.f, 0.f};
             if (j0 + j >= a.top_k || at < 0 || at >= a.rows) {
                 w[j] = 0.0f;  // nothing: 0 * 0
-            } else if constexpr (VEC) {
-                h[j] = *reinterpret_cast<const f32x4*>(a.h + at * a.n + n0);
+            } else if (whole) {
+                h[j] = *reinterpret_cast<const c4f*>(a.h + at * a.n + n0);
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 3; ++e)
                     if (n0 + e < a.n) h[j][e] = a.h[at * a.n + n0 + e];
             }
         }
@@ -608,16 +613,16 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
             for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(w[j], h[j][e], s[e]);
     }
     const int64_t at = t * a.n + n0;
-    if constexpr (VEC) {
+    if (whole) {
         if constexpr (YT == 0) {
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = s;
+            *reinterpret_cast<c4f*>(static_cast<float*>(a.y) + at) = s;
         } else {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-                make_uint2(f32_to_bf16(s[0]) | (f32_to_bf16(s[1]) << 16), f32_to_bf16(s[2]) | (f32_to_bf16(s[3]) << 16));
+            *reinterpret_cast<c4h*>(static_cast<uint16_t*>(a.y) + at) =
+                c4h{f32_to_bf16(s[0]) | (f32_to_bf16(s[1]) << 16), f32_to_bf16(s[2]) | (f32_to_bf16(s[3]) << 16)};
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 3; ++e)
             if (n0 + e < a.n) store_y<YT>(a.y, at + e, s[e]);
     }
 }
@@ -629,16 +634,10 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
     const int threads = a.tokens * ((a.n + 1023) / 1024) < 1024 ? kWave : kThreads;
     p.cols = 4 * threads;
     p.nblocks = (a.n + p.cols - 1) / p.cols;
-    const bool vec = a.n % 4 == 0;
     return launch_blocks(a.tokens * p.nblocks, threads, [&](uint32_t grid, int64_t block0) {
         p.block0 = block0;
-        if (a.yt == 0) {
-            if (vec) combine_kernel<0, true><<<grid, threads, 0, st>>>(p);
-            else combine_kernel<0, false><<<grid, threads, 0, st>>>(p);
-        } else {
-            if (vec) combine_kernel<1, true><<<grid, threads, 0, st>>>(p);
-            else combine_kernel<1, false><<<grid, threads, 0, st>>>(p);
-        }
+        if (a.yt == 0) combine_kernel<0><<<grid, threads, 0, st>>>(p);
+        else combine_kernel<1><<<grid, threads, 0, st>>>(p);
     });
 }
 

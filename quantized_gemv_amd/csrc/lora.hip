@@ -138,7 +138,10 @@ __device__ __forceinline__ void write_y(T v, T* p) {
     if constexpr (NT) __builtin_nontemporal_store(v, p);
     else *p = v;
 }
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// Four columns of y, aligned to their elements only (rows of any length start
+// anywhere): one load or store all the same, the memory system takes them.
+typedef float y4f __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t y4h __attribute__((ext_vector_type(2), aligned(2)));
 
 template <int YT, int MT, int KC, int CT>
 __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel(LoraParams p) {
@@ -162,61 +165,45 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const bool vec = (n & 3) == 0;  // whole 4-column pieces, aligned
 
+    typedef typename std::conditional<YT == 0, y4f, y4h>::type y_t;
     struct Block {
         u32x4 b[CT][KC];
-        float y[YR][4];
+        y_t y[YR];
     };
-    // y: thread (row tid / TPR + RPP s, columns 4 (tid % TPR) .. + 3; one by one
-    // tid % TPR + TPR e where n is no multiple of 4)
-    const int ycol = tid % TPR;
+    // y: thread (row tid / TPR + RPP s, four columns from 4 (tid % TPR), at the
+    // row's end its last four).  Every load is made, rows and columns past the
+    // ends repeat others and are not stored: loads under branches would be
+    // waited for one by one.
+    const int ycol = 4 * (tid % TPR);
     int64_t yat[YR];
+    uint32_t live = 0;
 #pragma unroll
     for (int s = 0; s < YR; ++s) {
         const int row = tid / TPR + RPP * s;
-        const int src = row < t.rows ? p.order[t.row0 + row] : -1;
-        yat[s] = src >= 0 && src < p.x_rows ? (int64_t)src * n : -1;
+        const int src = p.order[t.row0 + min(row, t.rows - 1)];
+        const bool in = src >= 0 && src < p.x_rows;
+        if (in && row < t.rows) live |= 1u << s;
+        yat[s] = in ? (int64_t)src * n : 0;
     }
     auto load = [&](int block_n, Block& k) {
         const int n0 = block_n * kXCols;
-        // B: lane (i, g) holds column i of a 16-column tile, ranks 8 (4 c + g) .. + 7
+        // B: lane (i, g) holds column i of a 16-column tile, ranks 8 (4 c + g) ..
+        // + 7; past the rank the first ones again, against zeros of v
 #pragma unroll
         for (int q = 0; q < CT; ++q) {
             const uint16_t* b = m.b + ((int64_t)t.group * n + min(n0 + 16 * (wave * CT + q) + i, n - 1)) * r;
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 const int at = (4 * c + g) * 8;
-                k.b[q][c] = u32x4{0u, 0u, 0u, 0u};
-                if (at < r) k.b[q][c] = *reinterpret_cast<const u32x4*>(b + at);
+                k.b[q][c] = *reinterpret_cast<const u32x4*>(b + (at < r ? at : 0));
             }
         }
+        const int at = min(n0 + ycol, n - 4);
 #pragma unroll
         for (int s = 0; s < YR; ++s) {
-            if (yat[s] < 0) continue;
-            if (vec) {
-                const int64_t at = yat[s] + n0 + 4 * ycol;
-                if (n0 + 4 * ycol < n) {
-                    if constexpr (YT == 0) {
-                        const f32x4 v = load_y<MT != 1>(reinterpret_cast<const f32x4*>(static_cast<const float*>(m.y) + at));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) k.y[s][e] = v[e];
-                    } else {
-                        const u32x2 v = load_y<MT != 1>(reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(m.y) + at));
-                        k.y[s][0] = bf16_to_f32(v.x & 0xFFFFu);
-                        k.y[s][1] = __uint_as_float(v.x & 0xFFFF0000u);
-                        k.y[s][2] = bf16_to_f32(v.y & 0xFFFFu);
-                        k.y[s][3] = __uint_as_float(v.y & 0xFFFF0000u);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t at = yat[s] + n0 + ycol + TPR * e;
-                    if (n0 + ycol + TPR * e < n)
-                        k.y[s][e] = YT == 0 ? static_cast<const float*>(m.y)[at] : bf16_to_f32(static_cast<const uint16_t*>(m.y)[at]);
-                }
-            }
+            if constexpr (YT == 0) k.y[s] = load_y<MT != 1>(reinterpret_cast<const y_t*>(static_cast<const float*>(m.y) + yat[s] + at));
+            else k.y[s] = load_y<MT != 1>(reinterpret_cast<const y_t*>(static_cast<const uint16_t*>(m.y) + yat[s] + at));
         }
     };
     auto finish = [&](int block_n, const Block& k) {
@@ -244,31 +231,34 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
             for (int q = 0; q < CT; ++q)
                 *reinterpret_cast<f32x4*>(dsh + (16 * a + i) * kXLine + 16 * (wave * CT + q) + 4 * g) = acc[a][q];
         lds_barrier();
+        const int at = min(n0 + ycol, n - 4), skip = n0 + ycol - at;  // 4 and more: a piece past the end
 #pragma unroll
         for (int s = 0; s < YR; ++s) {
-            if (yat[s] < 0) continue;
+            // the columns' products (those of a shifted piece start earlier, or in
+            // the block before: not stored)
             const float* line = dsh + (tid / TPR + RPP * s) * kXLine;
-            if (vec) {
-                const int64_t at = yat[s] + n0 + 4 * ycol;
-                if (n0 + 4 * ycol < n) {
-                    f32x4 v = *reinterpret_cast<const f32x4*>(line + 4 * ycol);
+            float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += k.y[s][e];
-                    if constexpr (YT == 0) {
-                        write_y<MT != 1>(v, reinterpret_cast<f32x4*>(static_cast<float*>(m.y) + at));
-                    } else {
-                        const u32x2 o = {f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16)};
-                        write_y<MT != 1>(o, reinterpret_cast<u32x2*>(static_cast<uint16_t*>(m.y) + at));
-                    }
+            for (int e = 0; e < 4; ++e) {
+                const float d = skip == 0 ? line[ycol + e] : line[max(at - n0 + e, 0)];
+                if constexpr (YT == 0) v[e] = k.y[s][e] + d;
+                else v[e] = ((e & 1) ? __uint_as_float(k.y[s][e >> 1] & 0xFFFF0000u) : bf16_to_f32(k.y[s][e >> 1] & 0xFFFFu)) + d;
+            }
+            if (!((live >> s) & 1)) continue;
+            if (skip == 0) {
+                if constexpr (YT == 0) {
+                    const y_t o = {v[0], v[1], v[2], v[3]};
+                    write_y<MT != 1>(o, reinterpret_cast<y_t*>(static_cast<float*>(m.y) + yat[s] + at));
+                } else {
+                    const y_t o = {f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16)};
+                    write_y<MT != 1>(o, reinterpret_cast<y_t*>(static_cast<uint16_t*>(m.y) + yat[s] + at));
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t at = yat[s] + n0 + ycol + TPR * e;
-                    if (n0 + ycol + TPR * e < n) {
-                        const float v = k.y[s][e] + line[ycol + TPR * e];
-                        if constexpr (YT == 0) static_cast<float*>(m.y)[at] = v;
-                        else static_cast<uint16_t*>(m.y)[at] = (uint16_t)f32_to_bf16(v);
+                for (int e = 1; e < 4; ++e) {
+                    if (e >= skip) {
+                        if constexpr (YT == 0) static_cast<float*>(m.y)[yat[s] + at + e] = v[e];
+                        else static_cast<uint16_t*>(m.y)[yat[s] + at + e] = (uint16_t)f32_to_bf16(v[e]);
                     }
                 }
             }

@@ -155,7 +155,7 @@ def test_validation_lora(qg):
     assert call(count=0) == ARG and call(count=9) == ARG and call(yt=2) == ARG
     assert call(g=groups(qg, per_row=2)) == SHAPE
     assert call(r=12) == SHAPE and call(r=0) == SHAPE and call(r=264) == SHAPE
-    assert call(n=0) == SHAPE and call(k=100) == SHAPE and call(x_rows=31) == SHAPE and call(x_rows=1 << 31) == SHAPE
+    assert call(n=0) == SHAPE and call(n=3) == SHAPE and call(k=100) == SHAPE and call(x_rows=31) == SHAPE and call(x_rows=1 << 31) == SHAPE
     assert call(a=U) == ALIGN and call(b=U) == ALIGN and call(y=U) == ALIGN and call(x=U) == ALIGN and call(ws=U) == ALIGN
     assert call(scale=U) == ALIGN
     assert call(ws=None) == WORKSPACE and call(nws=15) == WORKSPACE

@@ -90,7 +90,8 @@ class Case:
 
 @pytest.mark.parametrize("ybf16", [False, True])
 @pytest.mark.parametrize("m,groups,k,mats,drop,runs", [
-    (1, 1, 128, [(8, 1)], 0.0, False),
+    (1, 1, 128, [(8, 4)], 0.0, False),
+    (40, 2, 128, [(8, 5), (16, 6), (8, 7), (8, 66), (8, 67), (8, 129), (8, 259)], 0.1, True),
     (1, 64, 4096, [(16, 4096)], 0.0, False),
     (2, 3, 256, [(24, 33)], 0.0, False),
     (16, 64, 1024, [(16, 300), (8, 40), (64, 17)], 0.0, False),
