@@ -796,7 +796,7 @@ qg_status qg_qgemm_experts_swiglu(const qg_experts* gate, const qg_experts* up, 
 
 size_t qg_experts_combine_workspace_bytes(int64_t rows, int64_t n) {
     if (rows < 1 || rows > QG_MAX_PLAN_ROWS || n < 1 || n >= ((int64_t)1 << 30) || !fits(rows, n)) return 0;
-    return (size_t)rows * (size_t)n * sizeof(float);
+    return (size_t)rows * (size_t)n * sizeof(float) + 16;  // rows are read four columns at a time
 }
 
 qg_status qg_qgemm_experts_combine(const qg_experts* w, const qg_row_groups* groups, int32_t amode, const void* x,

@@ -171,8 +171,7 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
             }
         }
     };
-    bool more = c0 < c1;
-    if (more) {
+    if (c0 < c1) {
         load_x(c0, s[0]);
 #pragma unroll
         for (int d = 1; d < D - 1; ++d) {
@@ -192,26 +191,24 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
             for (int r = 0; r < 4; ++r)
                 sw[q][r] = p.scale[q][(int64_t)t.group * p.n + min(16 * (ot0 + wave) + 4 * g + r, p.n - 1)];
     }
-    for (int c = c0; more;) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (!more) break;
-            const int next = c + (D - 1) * U;
-            if (D > 1 && next < c1) {
-                load_w(next, s[(d + D - 1) % D]);
-                load_x(next, s[(d + D - 1) % D]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(s[d]);
-            __builtin_amdgcn_sched_barrier(0);
-            c += U;
-            more = c < c1;
-            if (D == 1 && more) {
-                load_w(c, s[0]);
-                load_x(c, s[0]);
-            }
+    auto step = [&](int c, int d, bool load) {  // d: c's set
+        if (load) {
+            load_w(c + (D - 1) * U, s[(d + D - 1) % D]);
+            load_x(c + (D - 1) * U, s[(d + D - 1) % D]);
         }
-    }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s[d]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // no branch between the loads and their products: a load that may or may
+    // not have been made is waited for as if it were the last one
+    int c = c0;
+    for (; c + (2 * D - 2) * U < c1; c += D * U)
+#pragma unroll
+        for (int d = 0; d < D; ++d) step(c + d * U, d, true);
+#pragma unroll
+    for (int d = 0; d < 2 * D - 2; ++d)
+        if (c + d * U < c1) step(c + d * U, d % D, c + (d + D - 1) * U < c1);
 #pragma unroll
     for (int q = 0; q < NT; ++q) part[wave][q][lane] = acc[q];
     lds_barrier();
@@ -586,44 +583,41 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
     const int64_t t = block / p.nblocks;
     const int64_t n0 = (block % p.nblocks) * p.cols + 4 * (int)threadIdx.x;
     if (n0 >= a.n) return;
-    const bool whole = n0 + 4 <= a.n;  // else the piece that the row ends in
+    // at the row's end its last four columns (a row of fewer: past it, into the
+    // workspace's padding); every load is made, slots and rows that are not
+    // there repeat others and count as zero
+    const int64_t at = max((int64_t)0, min(n0, a.n - 4)), skip = n0 - at;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < a.top_k; j0 += S) {
         f32x4 h[S];
         float w[S];
+        int64_t row[S];
 #pragma unroll
         for (int j = 0; j < S; ++j) {
             const int64_t slot = t * a.top_k + min(j0 + j, a.top_k - 1);
-            const int64_t at = a.pos[slot];
+            row[j] = a.pos[slot];
             w[j] = a.weights[slot];
-            h[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (j0 + j >= a.top_k || at < 0 || at >= a.rows) {
-                w[j] = 0.0f;  // nothing: 0 * 0
-            } else if (whole) {
-                h[j] = *reinterpret_cast<const c4f*>(a.h + at * a.n + n0);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (n0 + e < a.n) h[j][e] = a.h[at * a.n + n0 + e];
-            }
+            if (j0 + j >= a.top_k || row[j] >= a.rows) row[j] = -1;
         }
+#pragma unroll
+        for (int j = 0; j < S; ++j) h[j] = *reinterpret_cast<const c4f*>(a.h + max(row[j], (int64_t)0) * a.n + at);
 #pragma unroll
         for (int j = 0; j < S; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(w[j], h[j][e], s[e]);
+            for (int e = 0; e < 4; ++e) s[e] = row[j] >= 0 ? __builtin_fmaf(w[j], h[j][e], s[e]) : s[e];
     }
-    const int64_t at = t * a.n + n0;
-    if (whole) {
+    const int64_t out = t * a.n + at;
+    if (skip == 0 && a.n >= 4) {
         if constexpr (YT == 0) {
-            *reinterpret_cast<c4f*>(static_cast<float*>(a.y) + at) = s;
+            *reinterpret_cast<c4f*>(static_cast<float*>(a.y) + out) = s;
         } else {
-            *reinterpret_cast<c4h*>(static_cast<uint16_t*>(a.y) + at) =
+            *reinterpret_cast<c4h*>(static_cast<uint16_t*>(a.y) + out) =
                 c4h{f32_to_bf16(s[0]) | (f32_to_bf16(s[1]) << 16), f32_to_bf16(s[2]) | (f32_to_bf16(s[3]) << 16)};
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (n0 + e < a.n) store_y<YT>(a.y, at + e, s[e]);
+        for (int e = 0; e < 4; ++e)
+            if (e >= skip && at + e < a.n) store_y<YT>(a.y, out + e, s[e]);
     }
 }
 

@@ -42,7 +42,7 @@ def test_workspace_sizes(qg):
     assert f(0, 16) == 0 and f(qg.QG_MAX_PLAN_ROWS + 1, 16) == 0 and f(5000, 0) == 0 and f(5000, 1025) == 0
     assert f(qg.QG_MAX_PLAN_ROWS, 1024) <= 64 * 1024 * 4
     f = qg.lib().qg_experts_combine_workspace_bytes
-    assert f(10, 33) == 10 * 33 * 4
+    assert f(10, 33) >= 10 * 33 * 4
     assert f(0, 33) == 0 and f(10, 0) == 0 and f(qg.QG_MAX_PLAN_ROWS, 1 << 29) == 0
     f = qg.lib().qg_lora_workspace_bytes
     m = (qg.CLora * 2)(qg.CLora(A, A, None, 64, 8, 0, A), qg.CLora(A, A, None, 64, 40, 0, A))

@@ -114,6 +114,8 @@ def check(full, y, live, want, tol, bf16, guard=64):
 
 SIZES = [  # t, e, top, k, n, spread, drop
     (1, 1, 1, 128, 1, "even", 0.0),
+    (9, 2, 2, 128, 3, "even", 0.2),
+    (9, 5, 3, 1152, 6, "skew", 0.2),
     (1, 8, 2, 256, 40, "even", 0.0),
     (2, 3, 1, 128, 16, "even", 0.5),
     (5, 4, 4, 384, 33, "even", 0.2),
