@@ -138,6 +138,9 @@ SIZES = [  # t, e, top, k, n, spread, drop
     # many rows, too few 128-row tiles to fill the card
     (500, 5, 3, 640, 440, "skew", 0.0),
     (333, 30, 5, 256, 391, "skew", 0.1),
+    # the most slots per token; more experts than a wave has lanes, many empty
+    (21, 20, 16, 128, 70, "even", 0.1),
+    (300, 1024, 3, 128, 18, "even", 0.0),
 ]
 
 
@@ -251,11 +254,63 @@ def test_weights_past_4_gib(qg):
         del y, got
 
 
+def test_x_past_4_gib(qg):
+    note("an x that passes 32-bit offsets")
+    k, rows = 262144, 8500
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device="cuda")
+    g = synth.rng(11)
+    at = [0, 17, 8191, 8192, rows - 1]
+    bits = synth.to_bf16_bits(synth.gaussian(g, (len(at), k), 1.0))
+    x[torch.tensor(at, device="cuda")] = dev_bf16(bits)
+    codes = g.integers(-127, 128, (1, 16, k)).astype(np.int8)
+    w = qg.QExperts(qg.QG_WFMT_INT8, 1, 16, k, dev(codes), torch.full((1, 16), 30000.0, device="cuda"))
+    plan = qg.group_rows(torch.zeros(rows, dtype=torch.int32, device="cuda"), 1)
+    y = host(qg.qgemm_experts(w, x, plan))
+    want = synth.bf16_bits_to_f32(bits).astype(np.float64) @ codes[0].astype(np.float64).T / 30000.0
+    assert np.abs(y[at] - want).max() <= TOL_F32 * np.abs(want).max()
+    rest = np.ones(rows, bool)
+    rest[at] = False
+    assert not y[rest].any()
+
+
+def test_very_wide_matrix(qg):
+    note("a matrix of more than 2^21 rows")
+    n, k, t = 2100003, 128, 200
+    g = synth.rng(12)
+    at = [0, 1, n // 2, n - 17, n - 1]
+    vals = g.integers(-127, 128, (len(at), k)).astype(np.int8)
+    codes = torch.zeros((1, n, k), dtype=torch.int8, device="cuda")
+    codes[0, torch.tensor(at, device="cuda")] = dev(vals)
+    w = qg.QExperts(qg.QG_WFMT_INT8, 1, n, k, codes, torch.full((1, n), 700.0, device="cuda"))
+    bits = synth.to_bf16_bits(synth.gaussian(g, (t, k), 1.0))
+    plan = qg.group_rows(torch.zeros(t, dtype=torch.int32, device="cuda"), 1)
+    y = qg.qgemm_experts(w, dev_bf16(bits), plan)
+    want = synth.bf16_bits_to_f32(bits).astype(np.float64) @ vals.astype(np.float64).T / 700.0
+    assert np.abs(host(y[:, torch.tensor(at, device="cuda")]) - want).max() <= TOL_F32 * np.abs(want).max()
+    assert int((y != 0).sum()) <= t * len(at)
+
+
+def test_two_streams_at_once(qg):
+    note("two combine calls on two streams")
+    c = [Case(qg, 64, 8, 2, 512, 200, act8, True, 60, spread="skew", gather=False) for act8 in (False, True)]
+    st = [torch.cuda.Stream() for _ in c]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for j in (0, 1):
+            with torch.cuda.stream(st[j]):
+                outs.append((j, qg.qgemm_experts_combine(c[j].w[0], c[j].xd, c[j].groups, dev(c[j].weights), s_x=c[j].sxd)))
+    torch.cuda.synchronize()
+    for j, y in outs:
+        want, tol = c[j].combine()
+        assert np.all(np.abs(host(y) - want) <= tol + 1e-37)
+
+
 def test_stream_and_graph(qg):
     note("expert feed-forward on another stream, captured and replayed")
-    for t, act8 in ((4, False), (300, True)):
+    for t, act8, f in ((4, False, 384), (300, True, 384), (1200, False, 2048), (1200, True, 2048)):
         g = synth.rng(t)
-        e, top, k, f = 8, 2, 256, 384
+        e, top, k = 8, 2, 256
         gate, up, down = (qg.tiled16_experts(qg.quantize_experts(dev(synth.gaussian(g, s, 0.05))))
                           for s in ((e, f, k), (e, f, k), (e, k, f)))
         x = dev_bf16(synth.to_bf16_bits(synth.gaussian(g, (t, k), 1.0)))

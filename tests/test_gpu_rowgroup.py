@@ -53,7 +53,7 @@ def check_plan(plan, offsets, order, pos):
 
 @pytest.mark.parametrize("rows,groups", [(1, 1), (1, 1024), (2, 3), (63, 5), (64, 64), (65, 2), (511, 129), (2047, 1000),
                                          (2048, 8), (2049, 8), (4096, 1024), (5000, 1), (70001, 77), (131072 + 5, 128),
-                                         (300001, 1024)])
+                                         (300001, 1024), (5000003, 1000)])
 @pytest.mark.parametrize("drop", [0.0, 0.3])
 def test_group_rows(qg, rows, groups, drop):
     note("group_rows %d rows, %d groups, drop %g" % (rows, groups, drop))
@@ -111,8 +111,17 @@ def logits_case(t, e, bf16, seed, masked=0.0):
     return dev(l), l
 
 
+def route_fast(l, top_k, renorm):
+    """The oracle's router by a stable numpy sort (for many finite tokens)."""
+    l = l.astype(np.float64)
+    ids = np.argsort(-l, axis=1, kind="stable")[:, :top_k].astype(np.int32)
+    p = np.exp(l - l.max(1, keepdims=True))
+    w = np.take_along_axis(p, ids.astype(np.int64), 1)
+    return ids, w / (w if renorm else p).sum(1, keepdims=True)
+
+
 def check_route(qg, x, l, top_k, renorm, out=None):
-    ids, w = R.moe_route(l, top_k, renorm)
+    ids, w = R.moe_route(l, top_k, renorm) if l.shape[0] <= 3000 else route_fast(l, top_k, renorm)
     r = qg.moe_route(x, top_k, renorm, out=out)
     assert np.array_equal(host(r.ids), ids)
     assert np.allclose(host(r.weights), w, rtol=RTOL_W, atol=ATOL_W)
@@ -122,7 +131,7 @@ def check_route(qg, x, l, top_k, renorm, out=None):
 
 @pytest.mark.parametrize("t,e,top_k", [(1, 1, 1), (1, 8, 2), (3, 64, 8), (16, 64, 8), (5, 65, 16), (33, 128, 6),
                                        (64, 129, 8), (100, 256, 1), (7, 257, 5), (20, 1024, 16), (257, 60, 4),
-                                       (700, 96, 8)])
+                                       (700, 96, 8), (70001, 8, 2), (2048, 16, 1), (2049, 16, 1), (65, 40, 16)])
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route(qg, t, e, top_k, bf16, renorm):
