@@ -843,7 +843,9 @@ qg_status qg_qgemm_experts_combine(const qg_experts* w, const qg_row_groups* gro
  * r % 8 == 0, 8 <= r <= QG_LORA_MAX_R (each matrix its own); k % 128 == 0,
  * 128 <= k <= QG_BATCH_MAX_K; 4 <= n < 2^30; rows <= x_rows < 2^31;
  * groups <= QG_MAX_ROW_GROUPS; x_rows * k, x_rows * n, groups * n * r and
- * groups * r * k <= 2^40.  a, b, x, y 16-B aligned.
+ * groups * r * k <= 2^40.  a, b, x, y 16-B aligned; two y that share bytes are
+ * QG_ERR_ARG.  Values that are not finite, in x, A, B or scale A x rounded to
+ * bf16, reach the outputs that they enter as NaN.
  * ws: qg_lora_workspace_bytes(...) bytes for the same m (its r), count,
  *     rows, groups and k, 16-B aligned; contents on entry do not matter.
  *     Calls that overlap on one workspace race.

@@ -852,6 +852,15 @@ qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* grou
         if (!aligned16(mj.a) || !aligned16(mj.b) || !aligned16(mj.y) || !aligned_to(mj.scale, 4)) return QG_ERR_ALIGN;
         a.m[j] = {static_cast<const uint16_t*>(mj.a), static_cast<const uint16_t*>(mj.b), mj.scale, mj.n, mj.r, mj.y};
     }
+    // Two matrices that add to the same elements would race.
+    const uintptr_t elem = yt == QG_F32 ? 4 : 2;
+    for (int32_t j = 1; j < count; ++j) {
+        for (int32_t i = 0; i < j; ++i) {
+            const uintptr_t yj = reinterpret_cast<uintptr_t>(m[j].y), yi = reinterpret_cast<uintptr_t>(m[i].y);
+            const uintptr_t len = elem * (uintptr_t)x_rows * (uintptr_t)(yj < yi ? m[j].n : m[i].n);
+            if ((yj < yi ? yi - yj : yj - yi) < len) return QG_ERR_ARG;
+        }
+    }
     const size_t need = qg_lora_workspace_bytes(m, count, groups->rows, groups->groups, k);
     if (!ws || need == 0 || ws_bytes < need) return QG_ERR_WORKSPACE;
     if (!aligned16(ws)) return QG_ERR_ALIGN;

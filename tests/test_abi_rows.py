@@ -168,3 +168,23 @@ def test_binding_refuses_host_tensors(qg):
         qg.moe_route(torch.zeros(4, 8), 2)
     with pytest.raises(ValueError):
         qg.QExperts(qg.QG_WFMT_INT8, 1, 16, 128, torch.zeros(1, 16, 128, dtype=torch.int8), torch.zeros(1, 16))
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("yt", [0, 1])
+def test_lora_outputs_must_not_share_bytes(qg, yt):
+    # 32 rows of 64 columns from A on; the other output starts inside, ends
+    # inside, is the same, or touches neither end
+    size = 32 * 64 * (2 if yt else 4)
+    f = qg.lib().qg_lora_add
+
+    def call(y0, y1, n0=64, n1=64):
+        m = (qg.CLora * 2)(qg.CLora(A, A, None, n0, 16, 0, y0), qg.CLora(A, A, None, n1, 16, 0, y1))
+        return f(m, 2, groups(qg, per_row=1), A, 32, 256, yt, None, 0, None)
+
+    base = 1 << 40
+    assert call(base, base) == ARG
+    assert call(base, base + size - 16) == ARG and call(base + size - 16, base) == ARG
+    assert call(base, base + 16, 64, 4) == ARG
+    # apart: the next check, of the missing workspace, answers
+    assert call(base, base + size) == WORKSPACE and call(base + size, base) == WORKSPACE
