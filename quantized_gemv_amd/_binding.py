@@ -1019,8 +1019,10 @@ class LoraAdapters:
 
 class LoraLaunch:
     """Pre-marshalled arguments of one qg_lora_add call: the adapters of
-    1..QG_MAX_GROUP projections of the same x, added to ys (kept alive by this
-    object, with a workspace); launch() enqueues it on x's current stream."""
+    1..QG_MAX_GROUP projections of the same x, as they are now, added to ys
+    (all kept alive by this object, with a workspace); launch() enqueues it on
+    x's current stream. Launches that may overlap need objects of their own:
+    they share ys and the workspace."""
 
     def __init__(self, x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters],
                  ys: Sequence[torch.Tensor], ws: Optional[torch.Tensor] = None):
@@ -1044,7 +1046,9 @@ class LoraLaunch:
                   ad.a.shape[1], 0, y.data_ptr()) for ad, y in zip(adapters, ys)])
         self.ws, self.nws = _workspace(ws, int(lib().qg_lora_workspace_bytes(self.m, n, m, groups.groups, k)), x)
         self.cg = groups.c_struct()
-        self.x, self.keep = x, (groups, list(adapters), list(ys))
+        # the tensors themselves: an adapter whose fields are set anew later does
+        # not take the memory away that these arguments point to
+        self.x, self.keep = x, (groups, [(ad.a, ad.b, ad.scale) for ad in adapters], list(ys))
         self.args = (self.m, n, ctypes.byref(self.cg), _ptr(x), m, k, _xt(ys[0]), _ptr(self.ws), self.nws)
 
     def launch(self):

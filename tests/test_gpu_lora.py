@@ -202,6 +202,42 @@ def test_stream_and_graph(qg):
         assert all(torch.equal(a, b) for a, b in zip(ys, want))
 
 
+def test_launch_keeps_its_tensors(qg):
+    note("an adapter's fields set anew after the launch object was made")
+    c = Case(qg, 24, 3, 256, [(16, 96)], False, 15)
+    launch = qg.LoraLaunch(c.xd, c.groups, c.ad, c.ys)
+    ad = c.ad[0]
+    shapes = [(ad.a.shape, ad.a.dtype), (ad.b.shape, ad.b.dtype), (ad.scale.shape, ad.scale.dtype)] \
+        if ad.scale is not None else [(ad.a.shape, ad.a.dtype), (ad.b.shape, ad.b.dtype)]
+    ad.a = ad.b = ad.scale = None
+    others = [torch.full(s, 7.0, dtype=d, device="cuda") for s, d in shapes for _ in range(4)]
+    launch.launch()
+    torch.cuda.synchronize()
+    c.check()
+    del others
+
+
+def test_values_that_are_not_finite_stay_in_their_rows(qg):
+    note("NaN and infinities in x and B")
+    m, k, n = 40, 256, 70
+    c = Case(qg, m, 3, k, [(24, n)], False, 16, drop=0.3)
+    with_a = np.flatnonzero(c.ids >= 0)
+    without = np.flatnonzero(c.ids < 0)
+    c.xd[int(with_a[0]), 5] = float("nan")
+    c.xd[int(with_a[1]), 6] = float("inf")
+    c.xd[int(without[0]), 7] = float("nan")
+    g = int(c.ids[with_a[2]])
+    c.ad[0].b[g, 11, 3] = float("inf")
+    qg.lora_add(c.xd, c.groups, c.ad, c.ys)
+    got = host(c.ys[0])
+    want, tol = c.want(0)
+    odd = np.zeros((m, n), bool)
+    odd[with_a[:2]] = True
+    odd[c.ids == g, 11] = True
+    assert np.all(np.isnan(got[odd]))
+    assert np.all(np.abs(got[~odd] - want[~odd]) <= tol[~odd])
+
+
 def test_refusals(qg):
     c = Case(qg, 8, 4, 256, [(16, 32)], False, 1)
     x, gr, ad, ys = c.xd, c.groups, c.ad, c.ys
@@ -218,6 +254,8 @@ def test_refusals(qg):
         qg.LoraAdapters(ad[0].a, ad[0].b[:, :, :8].contiguous())
     with pytest.raises(qg.QgError):
         qg.lora_add(x, gr, [qg.LoraAdapters(ad[0].a[:, :12].contiguous(), ad[0].b[:, :, :12].contiguous())], ys)
+    with pytest.raises(qg.QgError):
+        qg.lora_add(x, gr, ad * 2, ys * 2)
     with pytest.raises(qg.QgError):
         qg.lora_add(x, gr, ad, ys, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(qg.QgError):
