@@ -738,7 +738,8 @@ qg_status qg_qgemm_w8a8(const int8_t* xq, const float* s_x, const void* x_out, i
  * qg_group_rows: ids, order, pos: [rows]; offsets: [groups + 1]; 1 <= rows <=
  *   QG_MAX_PLAN_ROWS, 1 <= groups <= QG_MAX_ROW_GROUPS.  ws:
  *   qg_group_rows_workspace_bytes(rows, groups) bytes, 16-B aligned (may be
- *   NULL when that is 0); its contents on entry do not matter.
+ *   NULL when that is 0); its contents on entry do not matter.  Outputs must not
+ *   overlap ids, one another or ws.
  */
 size_t qg_group_rows_workspace_bytes(int64_t rows, int32_t groups);  /* 0 if out of range, too */
 qg_status qg_group_rows(const int32_t* ids, int64_t rows, int32_t groups, int32_t* offsets, int32_t* order,
@@ -809,7 +810,8 @@ typedef struct qg_experts {
  *   per_row, in order, of weights[t][j] * (product row pos[t * per_row + j]);
  *   pos outside [0, rows) adds nothing.  pos, weights: [tokens][per_row];
  *   rows = tokens * per_row.  The products are held in fp32 in ws
- *   (qg_experts_combine_workspace_bytes(rows, n) bytes, 16-B aligned).
+ *   (qg_experts_combine_workspace_bytes(rows, n) bytes, 16-B aligned; calls that
+ *   overlap on one workspace race, here as in qg_group_rows and qg_moe_route).
  * Results of one call are deterministic; which kernel runs depends on the
  * sizes alone, and kernels differ in summation order.
  *

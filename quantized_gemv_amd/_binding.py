@@ -886,7 +886,8 @@ def quantize_experts(w: torch.Tensor) -> QExperts:
     if w.dim() != 3:
         raise ValueError("w must be [e][n][k]")
     e, n, k = w.shape
-    q, s = quantize_absmax(w.view(e * n, k), per_row=True)
+    with torch.cuda.device(w.device):
+        q, s = quantize_absmax(w.view(e * n, k), per_row=True)
     return QExperts(QG_WFMT_INT8, e, n, k, q.view(e, n, k), s.view(e, n))
 
 
@@ -900,8 +901,9 @@ def tiled16_experts(w: QExperts) -> QExperts:
         raise ValueError("shape (%d, %d) has no 16-row tiled layout" % (w.n, w.k))
     out = torch.empty((w.e, nb), dtype=torch.int8, device=w.codes.device)
     codes = w.codes.view(w.e, w.n, w.k)
-    for j in range(w.e):
-        pack_tiles16(codes[j], out[j])
+    with torch.cuda.device(codes.device):
+        for j in range(w.e):
+            pack_tiles16(codes[j], out[j])
     return QExperts(QG_WFMT_INT8_T16, w.e, w.n, w.k, out, w.scale)
 
 
@@ -917,6 +919,8 @@ def _experts_x(w: QExperts, x: torch.Tensor, groups: RowGroups, s_x: Optional[to
         _dev(s_x, "s_x", torch.float32)
         if s_x.numel() != x.shape[0]:
             raise ValueError("s_x must hold one scale per row of x")
+    if groups.per_row < 1:
+        raise ValueError("the plan's per_row is %d" % groups.per_row)
     want = -(-groups.rows // groups.per_row) if gather else groups.rows
     if x.shape[0] != want:
         raise ValueError("x has %d rows, the plan reads %d" % (x.shape[0], want))
@@ -990,10 +994,12 @@ def moe_ffn(x: torch.Tensor, logits: torch.Tensor, gate: QExperts, up: QExperts,
     r = moe_route(logits, top_k, renorm)
     s_x = s_h = None
     if act_int8:
-        x, s_x = quantize_absmax(x, per_row=True)
+        with torch.cuda.device(x.device):
+            x, s_x = quantize_absmax(x, per_row=True)
     h = qgemm_experts_swiglu(gate, up, x, r.groups, s_x=s_x)
     if act_int8:
-        h, s_h = quantize_absmax(h, per_row=True)
+        with torch.cuda.device(h.device):
+            h, s_h = quantize_absmax(h, per_row=True)
     return qgemm_experts_combine(down, h, r.groups, r.weights, s_x=s_h, y_dtype=y_dtype)
 
 

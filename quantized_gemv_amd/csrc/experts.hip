@@ -64,9 +64,9 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 // rows (GLU: 16 of the gate and the same 16 of the up matrix); each of its
 // four waves takes a quarter of k, two 16 x 16 tiles of
 // v_mfma_f32_16x16x32_bf16 (or v_mfma_i32_16x16x64_i8) that share the x
-// fragments, and their sums meet in LDS in order.  A unit of 64 k is loaded
-// while the one before it is multiplied, and the first codes are requested
-// before the rows of x are known.  Codes are read in whole 128-byte lines
+// fragments, and their sums meet in LDS in order.  Tiled codes: two units of
+// 64 k are on their way while one is multiplied, and the first codes are
+// requested before the rows of x are known.  Codes are read in whole 128-byte lines
 // (row-major: a pair of units at a time; tiled: blocks of 1 KB), once each:
 // non-temporal.
 //
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
     constexpr int OT = GLU ? 1 : NT;      // 16-row output tiles
     constexpr int U = TILED ? 1 : 2;      // units loaded together: row-major lines hold two
     // sets of registers, D - 1 of them on their way while one is multiplied
-    // (row-major: one set, reloaded after its products, and more waves)
+    // (row-major: one set, loaded and multiplied, and more waves instead)
     constexpr int D = TILED ? 3 : 1;
     constexpr int XF = ACT == 0 ? 2 : 1;  // x loads per unit and 16 rows
     typedef typename std::conditional<ACT == 0, f32x4, i32x4>::type acc_t;
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
                 s.w[q][u] = __builtin_amdgcn_raw_buffer_load_b128(rw[q], woff[q][u], c * (TILED ? 1024 : 64), kCachePolicyNT);
     };
     Units s[D];
-    if (c0 < c1) load_w(c0, s[0]);
+    if (D > 1 && c0 < c1) load_w(c0, s[0]);
     __builtin_amdgcn_sched_barrier(0);
     // this lane's x row (rows past the tile repeat its last)
     constexpr int kX = ACT == 0 ? 2 : 1;  // bytes of an x value
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
             }
         }
     };
-    if (c0 < c1) {
+    if (D > 1 && c0 < c1) {
         load_x(c0, s[0]);
 #pragma unroll
         for (int d = 1; d < D - 1; ++d) {

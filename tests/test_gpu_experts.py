@@ -379,6 +379,8 @@ def test_refusals(qg):
     with pytest.raises(ValueError):
         qg.qgemm_experts(w, x, gr, gather=False)
     with pytest.raises(ValueError):
+        qg.qgemm_experts(w, x, qg.RowGroups(gr.offsets, gr.order, gr.pos, 0))
+    with pytest.raises(ValueError):
         qg.qgemm_experts(w, x, gr, y_dtype=torch.float16)
     with pytest.raises(ValueError):
         qg.qgemm_experts(w, x, gr, y=torch.empty((15, 32), device="cuda"))
