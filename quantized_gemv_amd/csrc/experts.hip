@@ -26,7 +26,8 @@ struct ExpertParams {
     const int32_t* order;
     void* y;
     int64_t expert_bytes;     // one expert's codes
-    int32_t e, n, k, rows, x_rows, per_row;
+    int32_t e, n, k, rows, x_rows;
+    RowDiv per_row;
     int32_t tiled;            // 16-row tiled codes (else row-major); a 16-row tile is 16 k bytes in both
     int64_t block0;           // workgroups of earlier launches of the same product
     int32_t ntiles;           // workgroup tiles along n
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
     // this lane's x row (rows past the tile repeat its last)
     constexpr int kX = ACT == 0 ? 2 : 1;  // bytes of an x value
     const int at = t.row0 + min(i, t.rows - 1);
-    const int src = min(max(p.order ? p.order[at] / p.per_row : at, 0), p.x_rows - 1);
+    const int src = min(p.order ? divide(max(p.order[at], 0), p.per_row) : at, p.x_rows - 1);
     const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + (int64_t)src * p.k * kX + 16 * U * kX * g;
     auto load_x = [&](int c, Units& s) {
 #pragma unroll
@@ -290,7 +291,7 @@ struct TileAcc<1> {
 
 template <int ACT, int YT, bool GLU, bool TILED, int BM, int MA>
 __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTile& t, int n0, uint8_t* smem,
-                                             const uint32_t (&xoff)[BM / 32]) {
+                                             const uint32_t (&xoff)[BM / 32], float sx_tid) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5;
@@ -375,6 +376,12 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     // the end the last stage again, into a slot that is not read), always in
     // this order: at its start at most x of c + 1, codes of c and x of c + 2
     // may be outstanding, which leaves x of c landed.
+    // the outputs' scales are requested here, before anything that is counted
+    float sw[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+        sw[b] = p.scale[GLU ? b : 0][(int64_t)t.group * p.n + min(c0 + (GLU ? 0 : 32 * b) + (lane & 31), p.n - 1)];
+    __builtin_amdgcn_sched_barrier(0);
     Codes wa, wb;
     load_x(0, 0, 1);
     load_x(1, 0, 1);
@@ -384,6 +391,8 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     __builtin_amdgcn_sched_barrier(0);
     load_x(2, 0, 1);
     __builtin_amdgcn_sched_barrier(0);
+    // read after the barriers of the k loop
+    if (ACT == 1 && tid < BM) reinterpret_cast<float*>(smem + kTStages * (BM * 128))[tid] = 1.0f / sx_tid;
     auto step = [&](int c, const Codes& now, Codes& next) {
         wait_vmcnt<kLoads + 2 * MA>();
         lds_barrier();  // every wave's share of x stage c is there, and no one reads stage c - 1 any more
@@ -423,7 +432,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
     for (int b = 0; b < 2; ++b) {
         const int col = c0 + (GLU ? 0 : 32 * b) + (lane & 31);
         yoff[b] = col < p.n ? (uint32_t)(4 * h) * line + (uint32_t)(col * kY) : 0x80000000u;
-        rsw[b] = 1.0f / p.scale[GLU ? b : 0][(int64_t)t.group * p.n + min(col, p.n - 1)];
+        rsw[b] = 1.0f / sw[b];
     }
 #pragma unroll
     for (int a = 0; a < MA; ++a) {
@@ -455,11 +464,12 @@ __global__ __launch_bounds__(kTThreads, BM == 32 ? 4 : 2) void experts_tile_kern
     // the tile: consecutive workgroups go to different XCDs, each XCD gets a
     // contiguous run of the tiles there are (the grid is sized for the most
     // there can be)
-    const int64_t total = (int64_t)count_row_tiles<BM>(p.offsets, p.e, p.rows) * p.ntiles;
+    const GroupTiles first = group_tiles<BM>(p.offsets, p.e, p.rows, 0, 0);
+    const int64_t total = (int64_t)count_row_tiles<BM>(p.offsets, p.e, p.rows, first) * p.ntiles;
     const int64_t block = p.block0 + blockIdx.x, per = (total + 7) >> 3;
     const int64_t at = (block & 7) * per + (block >> 3);
     if ((block >> 3) >= per || at >= total) return;
-    RowTile t = find_row_tile<BM>(p.offsets, p.e, p.rows, (int)(at / p.ntiles));
+    RowTile t = find_row_tile<BM>(p.offsets, p.e, p.rows, (int)(at / p.ntiles), first);
     if (t.rows <= 0) return;
     const int64_t r = at - (int64_t)t.before * p.ntiles;
     const int mt = (t.count + BM - 1) / BM;
@@ -470,29 +480,31 @@ __global__ __launch_bounds__(kTThreads, BM == 32 ? 4 : 2) void experts_tile_kern
     t.row0 = t.first + m * BM;
     t.rows = min(BM, t.count - m * BM);
 
-    // rows past the tile repeat its last row
-    auto source = [&](int row) {
-        const int i = t.row0 + min(row, t.rows - 1);
-        const int src = p.order ? p.order[i] / p.per_row : i;
-        return min(max(src, 0), p.x_rows - 1);
-    };
-    uint32_t xsrc[BM / 32];
+    // rows of x of this lane's loads and (the last) of this thread's s_x; rows
+    // past the tile repeat its last.  All are requested before one is used.
+    constexpr int kL = BM / 32;
+    auto row_of = [&](int l) { return l < kL ? (wave + 4 * l) * 8 + (lane >> 3) : min(tid, BM - 1); };
+    int src[kL + ACT];
 #pragma unroll
-    for (int l = 0; l < BM / 32; ++l) {
-        const int row = (wave + 4 * l) * 8 + (lane >> 3);
-        xsrc[l] = (uint32_t)source(row) * (uint32_t)(p.k * (ACT == 0 ? 2 : 1)) + 16 * swz<8>(row, lane & 7);
+    for (int l = 0; l < kL + ACT; ++l) src[l] = t.row0 + min(row_of(l), t.rows - 1);
+    if (p.order) {
+#pragma unroll
+        for (int l = 0; l < kL + ACT; ++l) src[l] = p.order[src[l]];
+#pragma unroll
+        for (int l = 0; l < kL + ACT; ++l) src[l] = divide(max(src[l], 0), p.per_row);
     }
-    if constexpr (ACT == 1) {
-        // read after the barriers of the k loop
-        if (tid < BM) reinterpret_cast<float*>(smem + kTStages * (BM * 128))[tid] = 1.0f / p.s_x[source(tid)];
-    }
+    uint32_t xsrc[kL];
+#pragma unroll
+    for (int l = 0; l < kL; ++l)
+        xsrc[l] = (uint32_t)min(src[l], p.x_rows - 1) * (uint32_t)(p.k * (ACT == 0 ? 2 : 1)) + 16 * swz<8>(row_of(l), lane & 7);
+    const float sx_tid = ACT == 1 ? p.s_x[min(src[kL + ACT - 1], p.x_rows - 1)] : 1.0f;
     if constexpr (BM == 32) {
-        experts_tile<ACT, YT, GLU, TILED, BM, 1>(p, t, n0, smem, xsrc);
+        experts_tile<ACT, YT, GLU, TILED, BM, 1>(p, t, n0, smem, xsrc, sx_tid);
     } else {
-        if (t.rows > 96) experts_tile<ACT, YT, GLU, TILED, BM, 4>(p, t, n0, smem, xsrc);
-        else if (t.rows > 64) experts_tile<ACT, YT, GLU, TILED, BM, 3>(p, t, n0, smem, xsrc);
-        else if (t.rows > 32) experts_tile<ACT, YT, GLU, TILED, BM, 2>(p, t, n0, smem, xsrc);
-        else experts_tile<ACT, YT, GLU, TILED, BM, 1>(p, t, n0, smem, xsrc);
+        if (t.rows > 96) experts_tile<ACT, YT, GLU, TILED, BM, 4>(p, t, n0, smem, xsrc, sx_tid);
+        else if (t.rows > 64) experts_tile<ACT, YT, GLU, TILED, BM, 3>(p, t, n0, smem, xsrc, sx_tid);
+        else if (t.rows > 32) experts_tile<ACT, YT, GLU, TILED, BM, 2>(p, t, n0, smem, xsrc, sx_tid);
+        else experts_tile<ACT, YT, GLU, TILED, BM, 1>(p, t, n0, smem, xsrc, sx_tid);
     }
 }
 
@@ -554,7 +566,7 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t st) {
     p.k = (int32_t)a.k;
     p.rows = (int32_t)a.rows;
     p.x_rows = (int32_t)a.x_rows;
-    p.per_row = a.per_row;
+    p.per_row = row_div(a.per_row);
     p.expert_bytes = a.t16 ? (a.n + 15) / 16 * 16 * a.k : a.n * a.k;
     p.tiled = a.t16;
     const bool glu = a.codes2 != nullptr;

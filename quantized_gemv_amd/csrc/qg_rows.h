@@ -36,31 +36,41 @@ struct RowTile {
     int first, count, before;
 };
 
+// 64 groups from `base`, one per lane: their rows, tiles of MT rows, and the
+// tiles up to and with them (`before`: of the groups before base).
+struct GroupTiles {
+    int lo, hi, tiles, incl;
+};
+template <int MT>
+__device__ __forceinline__ GroupTiles group_tiles(const int32_t* __restrict__ offsets, int groups, int rows, int base,
+                                                  int before) {
+    const int g = base + (threadIdx.x & (kWave - 1));
+    GroupTiles t = {0, 0, 0, 0};
+    if (g < groups) {
+        t.lo = min(max(offsets[g], 0), rows);
+        t.hi = min(max(offsets[g + 1], t.lo), rows);
+    }
+    t.tiles = (t.hi - t.lo + MT - 1) / MT;
+    t.incl = before + wave_scan_incl(t.tiles);
+    return t;
+}
+
 // The tile-th tile of MT rows over all groups in ascending order, found by
 // one wave (all lanes active; the result is uniform): lane l takes group
 // base + l, the wave's prefix sum of their tile counts places the tile.
-// Groups without rows have no tiles.
+// Groups without rows have no tiles.  first: group_tiles of base 0.
 template <int MT>
-__device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int tile) {
-    const int lane = threadIdx.x & (kWave - 1);
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int tile,
+                                                 GroupTiles g) {
     RowTile t = {0, 0, 0, 0, 0, 0};
-    int before = 0;
-    for (int base = 0; base < groups; base += kWave) {
-        const int g = base + lane;
-        int lo = 0, hi = 0;
-        if (g < groups) {
-            lo = min(max(offsets[g], 0), rows);
-            hi = min(max(offsets[g + 1], lo), rows);
-        }
-        const int tiles = (hi - lo + MT - 1) / MT;
-        const int incl = before + wave_scan_incl(tiles);
-        const uint64_t hit = __ballot(tile >= incl - tiles && tile < incl);
+    for (int base = 0;;) {
+        const uint64_t hit = __ballot(tile >= g.incl - g.tiles && tile < g.incl);
         if (hit) {
             const int l = __builtin_ctzll(hit);
             t.group = base + l;
-            const int first = __builtin_amdgcn_readlane(lo, l);
-            const int last = __builtin_amdgcn_readlane(hi, l);
-            t.before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l);
+            const int first = __builtin_amdgcn_readlane(g.lo, l);
+            const int last = __builtin_amdgcn_readlane(g.hi, l);
+            t.before = __builtin_amdgcn_readlane(g.incl, l) - __builtin_amdgcn_readlane(g.tiles, l);
             const int at = tile - t.before;
             t.first = first;
             t.count = last - first;
@@ -68,7 +78,9 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
             t.rows = min(MT, last - t.row0);
             break;
         }
-        before = __builtin_amdgcn_readlane(incl, kWave - 1);
+        base += kWave;
+        if (base >= groups) break;
+        g = group_tiles<MT>(offsets, groups, rows, base, __builtin_amdgcn_readlane(g.incl, kWave - 1));
     }
     t.group = __builtin_amdgcn_readfirstlane(t.group);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
@@ -78,21 +90,31 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
     t.before = __builtin_amdgcn_readfirstlane(t.before);
     return t;
 }
-
-// Tiles of MT rows over all groups (uniform; all lanes active).
 template <int MT>
-__device__ __forceinline__ int count_row_tiles(const int32_t* __restrict__ offsets, int groups, int rows) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int sum = 0;
-    for (int base = 0; base < groups; base += kWave) {
-        const int g = base + lane;
-        if (g < groups) {
-            const int lo = min(max(offsets[g], 0), rows);
-            sum += (min(max(offsets[g + 1], lo), rows) - lo + MT - 1) / MT;
-        }
-    }
-    return wave_sum(sum);
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int tile) {
+    return find_row_tile<MT>(offsets, groups, rows, tile, group_tiles<MT>(offsets, groups, rows, 0, 0));
 }
+
+// Tiles of MT rows over all groups (uniform; all lanes active); first as above.
+template <int MT>
+__device__ __forceinline__ int count_row_tiles(const int32_t* __restrict__ offsets, int groups, int rows, GroupTiles g) {
+    for (int base = kWave; base < groups; base += kWave)
+        g = group_tiles<MT>(offsets, groups, rows, base, __builtin_amdgcn_readlane(g.incl, kWave - 1));
+    return __builtin_amdgcn_readlane(g.incl, kWave - 1);
+}
+
+// v / d for 0 <= v < 2^31 and d in [1, 16] by one product: mul = 2^shift / d
+// rounded up, 2^(shift - 31) >= d, so v (mul d - 2^shift) < 2^shift.
+struct RowDiv {
+    uint32_t mul;
+    int32_t shift;
+};
+inline RowDiv row_div(int d) {
+    int s = 31;
+    while ((1 << (s - 31)) < d) ++s;
+    return {(uint32_t)((((uint64_t)1 << s) + d - 1) / d), s};
+}
+__device__ __forceinline__ int divide(int v, const RowDiv& d) { return (int)(((uint64_t)(uint32_t)v * d.mul) >> d.shift); }
 
 // Most tiles of MT rows that `rows` rows in `groups` groups can make: every
 // group that has rows may end in a part tile.
