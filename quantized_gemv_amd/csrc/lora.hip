@@ -2,8 +2,9 @@
 //   y[t] += scale[g] B[g] (A[g] x[t]),  g the adapter of row t,
 // for up to 8 matrices that read the same x (q, k, v; gate, up).
 //
-// Two launches.  shrink: v = A x; a workgroup takes 16 sorted rows of one
-// adapter, one part of k and one matrix, on v_mfma_f32_16x16x32_bf16 (exact
+// Two launches.  shrink: v = A x; a workgroup takes 16 sorted rows (32 where the
+// groups have that many: A is read half as often; two of 2048 x 2048, rank 128,
+// 2048 rows: 57 -> 54 us) of one adapter, one part of k and one matrix, on v_mfma_f32_16x16x32_bf16 (exact
 // products, fp32 sums), and stores its fp32 partial sums [part][row][rank];
 // few rows would leave most CUs idle without the parts.  expand: the parts
 // are added in order, scaled and split into three bf16 terms (hi + mid + lo,
@@ -50,31 +51,36 @@ constexpr int kSWaves = 8;
 constexpr int kSThreads = kSWaves * kWave;
 constexpr int kSRanks = 64;  // ranks of a workgroup
 
-template <int RT>
+template <int RM, int RT>
 __device__ __forceinline__ void shrink_tile(const LoraParams& p, const LoraMatP& m, const RowTile& t, int kpart, int rg,
-                                            f32x4 (&red)[kSWaves][4][kWave]) {
+                                            f32x4 (&red)[kSWaves][RM * 4][kWave]) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int share = kpart * kSWaves + wave, shares = p.parts * kSWaves;
     const int units = p.k / 32;
     const int c0 = (int)((int64_t)units * share / shares), c1 = (int)((int64_t)units * (share + 1) / shares);
-    const int src = min(max(p.order[t.row0 + min(i, t.rows - 1)], 0), p.x_rows - 1);
-    const uint16_t* x = p.x + (int64_t)src * p.k + 8 * g;
+    const uint16_t* x[RM];
     const uint16_t* a[RT];
-    f32x4 acc[RT];
+    f32x4 acc[RM][RT];
 #pragma unroll
-    for (int q = 0; q < RT; ++q) {
-        a[q] = m.a + ((int64_t)t.group * m.r + min(kSRanks * rg + 16 * q + i, m.r - 1)) * p.k + 8 * g;
-        acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < RM; ++s) {
+        const int src = min(max(p.order[t.row0 + min(16 * s + i, t.rows - 1)], 0), p.x_rows - 1);
+        x[s] = p.x + (int64_t)src * p.k + 8 * g;
+#pragma unroll
+        for (int q = 0; q < RT; ++q) acc[s][q] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+        a[q] = m.a + ((int64_t)t.group * m.r + min(kSRanks * rg + 16 * q + i, m.r - 1)) * p.k + 8 * g;
     // the loads of several steps are requested together
     auto batch = [&](int c, auto steps) {
         constexpr int U = decltype(steps)::value;
-        u32x4 xf[U], af[U][RT];
+        u32x4 xf[U][RM], af[U][RT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            xf[u] = *reinterpret_cast<const u32x4*>(x + (c + u) * 32);
+#pragma unroll
+            for (int s = 0; s < RM; ++s) xf[u][s] = *reinterpret_cast<const u32x4*>(x[s] + (c + u) * 32);
 #pragma unroll
             for (int q = 0; q < RT; ++q) af[u][q] = *reinterpret_cast<const u32x4*>(a[q] + (c + u) * 32);
         }
@@ -82,9 +88,11 @@ __device__ __forceinline__ void shrink_tile(const LoraParams& p, const LoraMatP&
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int q = 0; q < RT; ++q)
-                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lbf16x8, af[u][q]),
-                                                                 __builtin_bit_cast(lbf16x8, xf[u]), acc[q], 0, 0, 0);
+            for (int s = 0; s < RM; ++s)
+#pragma unroll
+                for (int q = 0; q < RT; ++q)
+                    acc[s][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lbf16x8, af[u][q]),
+                                                                        __builtin_bit_cast(lbf16x8, xf[u][s]), acc[s][q], 0, 0, 0);
     };
     constexpr int U = RT == 4 ? 4 : 8;
     int c = c0;
@@ -92,21 +100,27 @@ __device__ __forceinline__ void shrink_tile(const LoraParams& p, const LoraMatP&
     for (; c + 2 <= c1; c += 2) batch(c, std::integral_constant<int, 2>());
     if (c < c1) batch(c, std::integral_constant<int, 1>());
 #pragma unroll
-    for (int q = 0; q < RT; ++q) red[wave][q][lane] = acc[q];
+    for (int s = 0; s < RM; ++s)
+#pragma unroll
+        for (int q = 0; q < RT; ++q) red[wave][s * RT + q][lane] = acc[s][q];
     lds_barrier();
+    // wave w finishes row tile w / RT, rank tile w % RT
     const int rpad = (m.r + 15) / 16 * 16;
-    if (wave < RT && kSRanks * rg + 16 * wave < rpad) {
+    const int row = 16 * (wave / RT) + i, rank = kSRanks * rg + 16 * (wave % RT);
+    if (wave < RM * RT && rank < rpad) {
         f32x4 s = red[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < kSWaves; ++w) s += red[w][wave][lane];
-        // lane l: sorted row l % 16, ranks 64 rg + 16 wave + 4 (l / 16) + r
-        if (i < t.rows)
-            *reinterpret_cast<f32x4*>(p.ws + m.ws_at + ((int64_t)kpart * p.rows + t.row0 + i) * rpad + kSRanks * rg + 16 * wave + 4 * g) = s;
+        // lane l: sorted row l % 16 of the tile, ranks 4 (l / 16) + r of the tile
+        if (row < t.rows)
+            *reinterpret_cast<f32x4*>(p.ws + m.ws_at + ((int64_t)kpart * p.rows + t.row0 + row) * rpad + rank + 4 * g) = s;
     }
 }
 
+template <int RM>
 __global__ __launch_bounds__(kSThreads) void lora_shrink_kernel(LoraParams p) {
-    __shared__ f32x4 red[kSWaves][4][kWave];
+    static_assert(RM * 4 <= kSWaves, "a wave per tile at the end");
+    __shared__ f32x4 red[kSWaves][RM * 4][kWave];
     int64_t block = p.block0 + blockIdx.x;
     const int mi = (int)(block % p.count);
     block /= p.count;
@@ -116,11 +130,11 @@ __global__ __launch_bounds__(kSThreads) void lora_shrink_kernel(LoraParams p) {
     const int ranks = m.r - kSRanks * rg;
     if (ranks <= 0) return;
     const int kpart = (int)(block % p.parts);
-    const RowTile t = find_row_tile<16>(p.offsets, p.groups, p.rows, (int)(block / p.parts));
+    const RowTile t = find_row_tile<16 * RM>(p.offsets, p.groups, p.rows, (int)(block / p.parts));
     if (t.rows <= 0) return;
-    if (ranks <= 16) shrink_tile<1>(p, m, t, kpart, rg, red);
-    else if (ranks <= 32) shrink_tile<2>(p, m, t, kpart, rg, red);
-    else shrink_tile<4>(p, m, t, kpart, rg, red);
+    if (ranks <= 16) shrink_tile<RM, 1>(p, m, t, kpart, rg, red);
+    else if (ranks <= 32) shrink_tile<RM, 2>(p, m, t, kpart, rg, red);
+    else shrink_tile<RM, 4>(p, m, t, kpart, rg, red);
 }
 
 // ------------------------------------------------------------------ expand
@@ -287,16 +301,16 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
         if (4 * j4 < r && row < t.rows) {
             const float* at = p.ws + m.ws_at + (int64_t)(t.row0 + row) * rpad + 4 * j4;
             const int64_t step = (int64_t)p.rows * rpad;
-            if (p.parts == 1) {
-                v = *reinterpret_cast<const f32x4*>(at);
-            } else {
-                f32x4 part[kLMaxParts];
+            auto add = [&](auto most) {  // up to that many parts, requested together
+                f32x4 part[decltype(most)::value];
 #pragma unroll
-                for (int s = 0; s < kLMaxParts; ++s) part[s] = *reinterpret_cast<const f32x4*>(at + min(s, p.parts - 1) * step);
+                for (int s = 0; s < most; ++s) part[s] = *reinterpret_cast<const f32x4*>(at + min(s, p.parts - 1) * step);
 #pragma unroll
-                for (int s = 0; s < kLMaxParts; ++s)
+                for (int s = 0; s < most; ++s)
                     if (s < p.parts) v += part[s];
-            }
+            };
+            if (p.parts <= 2) add(std::integral_constant<int, 2>());
+            else add(std::integral_constant<int, kLMaxParts>());
         }
         uint32_t term[3][4];
 #pragma unroll
@@ -325,10 +339,18 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
     }
 }
 
-// Parts of k of the shrink: enough workgroups to fill the CUs.
+// 32 rows per workgroup where the groups have that many.
+static bool tall_groups(int64_t rows, int64_t groups) { return rows >= 32 * groups; }
+static int shrink_rows(int64_t rows, int64_t groups) { return tall_groups(rows, groups) ? 32 : 16; }
+
+// Parts of k of the shrink: enough workgroups to fill the CUs, and a
+// workgroup's own time kept short: 2048 of k at most (us with the expand, one
+// part for all of k and this: 4129 rows, 8192 x 4096, rank 64: 81, 75; 700 rows
+// of 100 adapters, two of 8192 x 1024: 24, 17; at 1024 of k 84 and 21).
 static int lora_parts(int64_t rows, int64_t groups, int64_t k, int count, int rmax) {
-    const int64_t blocks = max_row_tiles(rows, groups, 16) * count * ((rmax + kSRanks - 1) / kSRanks);
+    const int64_t blocks = max_row_tiles(rows, groups, shrink_rows(rows, groups)) * count * ((rmax + kSRanks - 1) / kSRanks);
     int64_t parts = (256 + blocks - 1) / blocks;
+    if (parts < (k + 2047) / 2048) parts = (k + 2047) / 2048;
     const int64_t most = k / 32 / kSWaves;  // a matrix instruction per wave at least
     if (parts > most) parts = most;
     if (parts > kLMaxParts) parts = kLMaxParts;
@@ -356,8 +378,7 @@ static hipError_t run_expand(LoraParams& p, int64_t widest, hipStream_t st) {
 }
 template <int YT>
 static hipError_t launch_expand(LoraParams& p, int rmax, int64_t widest, hipStream_t st) {
-    // 32 rows per workgroup where the groups have that many
-    const bool tall = p.rows >= 32 * (int64_t)p.groups;
+    const bool tall = tall_groups(p.rows, p.groups);
     if (rmax <= 32) return tall ? run_expand<YT, 2, 1, 2>(p, widest, st) : run_expand<YT, 1, 1, 4>(p, widest, st);
     if (rmax <= 64) return tall ? run_expand<YT, 2, 2, 2>(p, widest, st) : run_expand<YT, 1, 2, 2>(p, widest, st);
     if (rmax <= 128) return tall ? run_expand<YT, 2, 4, 2>(p, widest, st) : run_expand<YT, 1, 4, 2>(p, widest, st);
@@ -387,10 +408,12 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t st) {
         at += (int64_t)p.parts * a.rows * ((m.r + 15) / 16 * 16);
         if (m.n > widest) widest = m.n;
     }
-    const hipError_t e = launch_blocks(max_row_tiles(a.rows, a.groups, 16) * p.parts * p.rgroups * p.count, kSThreads,
+    const int tile = shrink_rows(a.rows, a.groups);
+    const hipError_t e = launch_blocks(max_row_tiles(a.rows, a.groups, tile) * p.parts * p.rgroups * p.count, kSThreads,
                                        [&](uint32_t grid, int64_t block0) {
                                            p.block0 = block0;
-                                           lora_shrink_kernel<<<grid, kSThreads, 0, st>>>(p);
+                                           if (tile == 32) lora_shrink_kernel<2><<<grid, kSThreads, 0, st>>>(p);
+                                           else lora_shrink_kernel<1><<<grid, kSThreads, 0, st>>>(p);
                                        });
     if (e != hipSuccess) return e;
     return a.yt == 0 ? launch_expand<0>(p, rmax, widest, st) : launch_expand<1>(p, rmax, widest, st);
