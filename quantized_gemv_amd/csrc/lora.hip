@@ -195,14 +195,16 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
     // waited for one by one.
     const int ycol = 4 * (tid % TPR);
     int64_t yat[YR];
+    int src[YR];
     uint32_t live = 0;
 #pragma unroll
+    for (int s = 0; s < YR; ++s) src[s] = p.order[t.row0 + min(tid / TPR + RPP * s, t.rows - 1)];
+    __builtin_amdgcn_sched_barrier(0);  // all requested before one is used
+#pragma unroll
     for (int s = 0; s < YR; ++s) {
-        const int row = tid / TPR + RPP * s;
-        const int src = p.order[t.row0 + min(row, t.rows - 1)];
-        const bool in = src >= 0 && src < p.x_rows;
-        if (in && row < t.rows) live |= 1u << s;
-        yat[s] = in ? (int64_t)src * n : 0;
+        const bool in = src[s] >= 0 && src[s] < p.x_rows;
+        live |= in && tid / TPR + RPP * s < t.rows ? 1u << s : 0u;
+        yat[s] = in ? (int64_t)src[s] * n : 0;
     }
     auto load = [&](int block_n, Block& k) {
         const int n0 = block_n * kXCols;
@@ -305,9 +307,12 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
                 f32x4 part[decltype(most)::value];
 #pragma unroll
                 for (int s = 0; s < most; ++s) part[s] = *reinterpret_cast<const f32x4*>(at + min(s, p.parts - 1) * step);
+                v = part[0];
 #pragma unroll
-                for (int s = 0; s < most; ++s)
-                    if (s < p.parts) v += part[s];
+                for (int s = 1; s < most; ++s) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += s < p.parts ? part[s][e] : 0.0f;  // under a branch the loads would follow
+                }
             };
             if (p.parts <= 2) add(std::integral_constant<int, 2>());
             else add(std::integral_constant<int, kLMaxParts>());
