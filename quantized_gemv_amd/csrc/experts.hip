@@ -266,8 +266,8 @@ static hipError_t run_stream(ExpertParams p, hipStream_t st) {
 // by all column tiles at a time, and each XCD takes one contiguous run of
 // that order, so the tiles that run together share codes and rows in its L2.
 //
-// 2048 tokens, 8 experts of 2 x 11008 x 4096, bf16 x: 704 us, 1.05 PFLOP/s.
-// What holds it, from runs with parts taken out: the matrix instructions alone
+// 2048 tokens, 8 experts of 2 x 11008 x 4096, bf16 x: 676 us, 1.09 PFLOP/s.
+// What holds it, from runs with parts taken out (at 704 us): the matrix instructions alone
 // take 453 us (the clock falls to 1.8 GHz under them), without the LDS reads
 // 597, without the widening 651, with neither x nor codes loaded 466: the loads
 // cost most.  They are not late (codes two stages ahead: no change) and not
@@ -275,7 +275,10 @@ static hipError_t run_stream(ExpertParams p, hipStream_t st) {
 // Tried and slower: 256 rows by eight waves, one workgroup per CU (796: fewer
 // bytes, but no second workgroup to cover the barrier), one, two, four row
 // tiles at a time (808, 750, 726 against 715 with eight).  Loads between the
-// products instead of before them and a raised wave priority: 3.5%.
+// products instead of before them and a raised wave priority: 3.5%.  y is
+// stored as the products leave it, 128 bytes of two rows at a time: four columns
+// of 32 rows at a time (operands swapped) was 3-10% slower, whole rows by way of
+// LDS 2-4%.
 constexpr int kTN = 256, kTThreads = 256, kTStages = 4;
 constexpr int kTall = 8;  // row tiles that go through the column tiles together
 constexpr size_t tile_lds(int bm) { return (size_t)kTStages * bm * 128 + bm * sizeof(float); }

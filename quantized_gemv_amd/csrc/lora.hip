@@ -4,16 +4,17 @@
 //
 // Two launches.  shrink: v = A x; a workgroup takes 16 sorted rows (32 where the
 // groups have that many: A is read half as often; two of 2048 x 2048, rank 128,
-// 2048 rows: 57 -> 54 us) of one adapter, one part of k and one matrix, on v_mfma_f32_16x16x32_bf16 (exact
-// products, fp32 sums), and stores its fp32 partial sums [part][row][rank];
-// few rows would leave most CUs idle without the parts.  expand: the parts
+// 2048 rows: 57 -> 54 us) of one adapter, one part of k and one matrix, on
+// v_mfma_f32_16x16x32_bf16 (exact products, fp32 sums), and stores its fp32
+// partial sums [part][row][rank]; few rows would leave most CUs idle without
+// the parts.  expand: the parts
 // are added in order, scaled and split into three bf16 terms (hi + mid + lo,
 // 24 bits: nothing of the fp32 value is lost), so that the product with B
 // runs on the same matrix instructions; y is read, added to and written once.
 //
 // Few rows: the latency of two dependent launches (16 rows, rank 16, 4096 x
-// 4096: 4.0 + 4.4 us).  Many: reading and writing y (4129 rows of 11008 fp32,
-// rank 64: 72 us for 364 MB, 5.1 TB/s, after 21 us of shrink).
+// 4096: 4.2 + 4.4 us).  Many: reading and writing y (4129 rows of 11008 fp32,
+// rank 64: 72 us for 364 MB, 5.1 TB/s, after 17 us of shrink).
 #include "qg_launch.h"
 #include "qg_rows.h"
 
