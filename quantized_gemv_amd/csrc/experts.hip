@@ -105,9 +105,10 @@ __global__ __launch_bounds__(kEThreads, 5) void experts_stream_kernel(ExpertPara
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;  // weight row / x row, k group
+    const GroupOffsets groups = request_groups(p.offsets, p.e, 0);
     const int64_t block = p.block0 + blockIdx.x;
     const int ot0 = (int)(block % p.ntiles) * OT;  // first 16-row output tile
-    const RowTile t = find_row_tile<16>(p.offsets, p.e, p.rows, (int)(block / p.ntiles));
+    const RowTile t = find_row_tile<16>(p.offsets, p.e, p.rows, (int)(block / p.ntiles), group_tiles<16>(groups, p.rows, 0));
     if (t.rows <= 0) return;  // uniform over the workgroup
 
     const int pairs = p.k / (2 * kEUnit);
@@ -467,7 +468,7 @@ __global__ __launch_bounds__(kTThreads, BM == 32 ? 4 : 2) void experts_tile_kern
     // the tile: consecutive workgroups go to different XCDs, each XCD gets a
     // contiguous run of the tiles there are (the grid is sized for the most
     // there can be)
-    const GroupTiles first = group_tiles<BM>(p.offsets, p.e, p.rows, 0, 0);
+    const GroupTiles first = group_tiles<BM>(request_groups(p.offsets, p.e, 0), p.rows, 0);
     const int64_t total = (int64_t)count_row_tiles<BM>(p.offsets, p.e, p.rows, first) * p.ntiles;
     const int64_t block = p.block0 + blockIdx.x, per = (total + 7) >> 3;
     const int64_t at = (block & 7) * per + (block >> 3);

@@ -122,6 +122,7 @@ template <int RM>
 __global__ __launch_bounds__(kSThreads) void lora_shrink_kernel(LoraParams p) {
     static_assert(RM * 4 <= kSWaves, "a wave per tile at the end");
     __shared__ f32x4 red[kSWaves][RM * 4][kWave];
+    const GroupOffsets groups = request_groups(p.offsets, p.groups, 0);
     int64_t block = p.block0 + blockIdx.x;
     const int mi = (int)(block % p.count);
     block /= p.count;
@@ -129,10 +130,9 @@ __global__ __launch_bounds__(kSThreads) void lora_shrink_kernel(LoraParams p) {
     block /= p.rgroups;
     const LoraMatP& m = p.m[mi];
     const int ranks = m.r - kSRanks * rg;
-    if (ranks <= 0) return;
     const int kpart = (int)(block % p.parts);
-    const RowTile t = find_row_tile<16 * RM>(p.offsets, p.groups, p.rows, (int)(block / p.parts));
-    if (t.rows <= 0) return;
+    const RowTile t = find_row_tile<16 * RM>(p.offsets, p.groups, p.rows, (int)(block / p.parts), group_tiles<16 * RM>(groups, p.rows, 0));
+    if (t.rows <= 0 || ranks <= 0) return;
     if (ranks <= 16) shrink_tile<RM, 1>(p, m, t, kpart, rg, red);
     else if (ranks <= 32) shrink_tile<RM, 2>(p, m, t, kpart, rg, red);
     else shrink_tile<RM, 4>(p, m, t, kpart, rg, red);
@@ -172,15 +172,15 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
     constexpr int YR = R / RPP;                 // passes
     __shared__ u32x4 vsh[3 * KG * R];           // v: [term][k group of 8][row]
     __shared__ __attribute__((aligned(16))) float dsh[R * kXLine];
+    const GroupOffsets groups = request_groups(p.offsets, p.groups, 0);
     const int64_t block = p.block0 + blockIdx.x;
     const int strip = (int)(block % p.strips), mi = (int)(block / p.strips % p.count);
     const LoraMatP& m = p.m[mi];
     const int n = m.n, r = m.r;
     const int nb1 = min((strip + 1) * p.strip_blocks, (n + kXCols - 1) / kXCols);
     int nb = strip * p.strip_blocks;
-    if (nb >= nb1) return;
-    const RowTile t = find_row_tile<R>(p.offsets, p.groups, p.rows, (int)(block / p.strips / p.count));
-    if (t.rows <= 0) return;
+    const RowTile t = find_row_tile<R>(p.offsets, p.groups, p.rows, (int)(block / p.strips / p.count), group_tiles<R>(groups, p.rows, 0));
+    if (t.rows <= 0 || nb >= nb1) return;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, g = lane >> 4;

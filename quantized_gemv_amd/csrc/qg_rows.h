@@ -41,15 +41,21 @@ struct RowTile {
 struct GroupTiles {
     int lo, hi, tiles, incl;
 };
-template <int MT>
-__device__ __forceinline__ GroupTiles group_tiles(const int32_t* __restrict__ offsets, int groups, int rows, int base,
-                                                  int before) {
+// request_groups only asks for the offsets (groups past the last are empty): a
+// kernel does it first and takes its block number apart while they come, with no
+// exit in between (16 rows with adapters of rank 16: 8.4 -> 8.0 us).
+struct GroupOffsets {
+    int lo, hi;
+};
+__device__ __forceinline__ GroupOffsets request_groups(const int32_t* __restrict__ offsets, int groups, int base) {
     const int g = base + (threadIdx.x & (kWave - 1));
-    GroupTiles t = {0, 0, 0, 0};
-    if (g < groups) {
-        t.lo = min(max(offsets[g], 0), rows);
-        t.hi = min(max(offsets[g + 1], t.lo), rows);
-    }
+    return {offsets[min(g, groups)], offsets[min(g + 1, groups)]};
+}
+template <int MT>
+__device__ __forceinline__ GroupTiles group_tiles(const GroupOffsets& o, int rows, int before) {
+    GroupTiles t;
+    t.lo = min(max(o.lo, 0), rows);
+    t.hi = min(max(o.hi, t.lo), rows);
     t.tiles = (t.hi - t.lo + MT - 1) / MT;
     t.incl = before + wave_scan_incl(t.tiles);
     return t;
@@ -58,7 +64,7 @@ __device__ __forceinline__ GroupTiles group_tiles(const int32_t* __restrict__ of
 // The tile-th tile of MT rows over all groups in ascending order, found by
 // one wave (all lanes active; the result is uniform): lane l takes group
 // base + l, the wave's prefix sum of their tile counts places the tile.
-// Groups without rows have no tiles.  first: group_tiles of base 0.
+// Groups without rows have no tiles.  g: group_tiles of base 0.
 template <int MT>
 __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int tile,
                                                  GroupTiles g) {
@@ -80,7 +86,7 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
         }
         base += kWave;
         if (base >= groups) break;
-        g = group_tiles<MT>(offsets, groups, rows, base, __builtin_amdgcn_readlane(g.incl, kWave - 1));
+        g = group_tiles<MT>(request_groups(offsets, groups, base), rows, __builtin_amdgcn_readlane(g.incl, kWave - 1));
     }
     t.group = __builtin_amdgcn_readfirstlane(t.group);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
@@ -90,16 +96,12 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
     t.before = __builtin_amdgcn_readfirstlane(t.before);
     return t;
 }
-template <int MT>
-__device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int tile) {
-    return find_row_tile<MT>(offsets, groups, rows, tile, group_tiles<MT>(offsets, groups, rows, 0, 0));
-}
 
-// Tiles of MT rows over all groups (uniform; all lanes active); first as above.
+// Tiles of MT rows over all groups (uniform; all lanes active); g as above.
 template <int MT>
 __device__ __forceinline__ int count_row_tiles(const int32_t* __restrict__ offsets, int groups, int rows, GroupTiles g) {
     for (int base = kWave; base < groups; base += kWave)
-        g = group_tiles<MT>(offsets, groups, rows, base, __builtin_amdgcn_readlane(g.incl, kWave - 1));
+        g = group_tiles<MT>(request_groups(offsets, groups, base), rows, __builtin_amdgcn_readlane(g.incl, kWave - 1));
     return __builtin_amdgcn_readlane(g.incl, kWave - 1);
 }
 
