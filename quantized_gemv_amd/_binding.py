@@ -1006,12 +1006,17 @@ def moe_ffn(x: torch.Tensor, logits: torch.Tensor, gate: QExperts, up: QExperts,
 @dataclass
 class LoraAdapters:
     """Low-rank adapters of one projection: a [groups][r][k] and b
-    [groups][n][r] bf16, scale fp32 [groups] or None (1)."""
+    [groups][n][r] bf16, scale fp32 [groups] or None (1). Fields may be set
+    anew: they are checked when the object is made and by every LoraLaunch."""
     a: torch.Tensor
     b: torch.Tensor
     scale: Optional[torch.Tensor] = None
 
     def __post_init__(self):
+        self.check()
+
+    def check(self):
+        """ValueError unless the fields, as they are now, fit together."""
         _dev(self.a, "a", torch.bfloat16)
         _dev(self.b, "b", torch.bfloat16)
         if self.a.dim() != 3 or self.b.dim() != 3 or self.a.shape[0] != self.b.shape[0] or self.a.shape[1] != self.b.shape[2]:
@@ -1042,6 +1047,7 @@ class LoraLaunch:
         m, k = x.shape
         for ad, y in zip(adapters, ys):
             _dev(y, "y", (torch.float32, torch.bfloat16))
+            ad.check()  # its fields may have been set anew
             _same_device(x, ad.a, y)
             if ad.a.shape[0] != groups.groups or ad.a.shape[2] != k:
                 raise ValueError("a must be [%d][r][%d]" % (groups.groups, k))
