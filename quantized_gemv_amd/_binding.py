@@ -1033,7 +1033,9 @@ class LoraLaunch:
     1..QG_MAX_GROUP projections of the same x, as they are now, added to ys
     (all kept alive by this object, with a workspace); launch() enqueues it on
     x's current stream. Launches that may overlap need objects of their own:
-    they share ys and the workspace."""
+    they share ys and the workspace. The object may be dropped while launches
+    run, on any stream; while a graph that captured one may be replayed, it has
+    to be kept."""
 
     def __init__(self, x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters],
                  ys: Sequence[torch.Tensor], ws: Optional[torch.Tensor] = None):
@@ -1057,6 +1059,8 @@ class LoraLaunch:
             CLora(ad.a.data_ptr(), ad.b.data_ptr(), None if ad.scale is None else ad.scale.data_ptr(), ad.b.shape[1],
                   ad.a.shape[1], 0, y.data_ptr()) for ad, y in zip(adapters, ys)])
         self.ws, self.nws = _workspace(ws, int(lib().qg_lora_workspace_bytes(self.m, n, m, groups.groups, k)), x)
+        # the stream that a workspace of this object's own comes from
+        self.made_on = None if self.ws is ws else _raw_stream(x.get_device())
         self.cg = groups.c_struct()
         # the tensors themselves: an adapter whose fields are set anew later does
         # not take the memory away that these arguments point to
@@ -1064,6 +1068,10 @@ class LoraLaunch:
         self.args = (self.m, n, ctypes.byref(self.cg), _ptr(x), m, k, _xt(ys[0]), _ptr(self.ws), self.nws)
 
     def launch(self):
+        if self.made_on is not None and _raw_stream(self.x.get_device()) != self.made_on:
+            # no one else knows of this use: once dropped, the workspace would go
+            # to the next tensor of its own stream while the kernels still run
+            self.ws.record_stream(torch.cuda.current_stream(self.x.device))
         _call("qg_lora_add", self.x, *self.args)
 
 

@@ -217,6 +217,26 @@ def test_launch_keeps_its_tensors(qg):
     del others
 
 
+def test_launch_on_another_stream_and_dropped(qg):
+    note("a launch object used on another stream than its own, dropped while its kernels wait")
+    c = Case(qg, 300, 4, 1024, [(32, 260), (16, 96)], False, 18, runs=True)
+    launch = qg.LoraLaunch(c.xd, c.groups, c.ad, c.ys)
+    size = launch.nws
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    m = torch.zeros((4096, 4096), device="cuda")
+    with torch.cuda.stream(st):
+        for _ in range(20):  # the launch waits behind these
+            torch.mm(m, m)
+        launch.launch()
+    del launch
+    # the first stream's next tensors of that size: none may be the workspace
+    others = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 0x5A).all()) for t in others)
+    c.check()
+
+
 def test_values_that_are_not_finite_stay_in_their_rows(qg):
     note("NaN and infinities in x and B")
     m, k, n = 40, 256, 70

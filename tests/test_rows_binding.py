@@ -22,6 +22,7 @@ def qg(monkeypatch):
         return t
 
     monkeypatch.setattr(q._binding, "_dev", dev)
+    monkeypatch.setattr(q._binding, "_raw_stream", lambda index: 7)
     return q
 
 
@@ -58,3 +59,31 @@ def test_launch_checks_adapters_as_they_are_now(qg, field, value):
     setattr(ad, field, value)
     with pytest.raises(ValueError):
         qg.LoraLaunch(x, plan(qg), [ad], ys)
+
+
+class Recorded:
+    """A workspace that notes the streams it is recorded on."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_workspace_is_recorded_on_other_streams(qg, monkeypatch):
+    """The workspace that a launch object takes by itself belongs to the stream
+    it was made on: the allocator has to hear of every other one."""
+    calls = []
+    monkeypatch.setattr(qg._binding, "_call", lambda name, x, *args: calls.append(name))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "stream %d" % qg._binding._raw_stream(-1))
+    x, ys = bf16(8, 256), [torch.zeros(8, 32)]
+    own = qg.LoraLaunch(x, plan(qg), [adapters(qg)], ys)
+    given = qg.LoraLaunch(x, plan(qg), [adapters(qg)], ys, ws=torch.zeros(1 << 16, dtype=torch.uint8))
+    own.ws, given.ws = Recorded(), Recorded()
+    for stream in (7, 9, 7, 8):
+        monkeypatch.setattr(qg._binding, "_raw_stream", lambda index: stream)
+        own.launch()
+        given.launch()
+    assert own.ws.streams == ["stream 9", "stream 8"] and given.ws.streams == []
+    assert calls == ["qg_lora_add"] * 8
