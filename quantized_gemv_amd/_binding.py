@@ -1062,24 +1062,31 @@ class LoraLaunch:
         # the stream that a workspace of this object's own comes from
         self.made_on = None if self.ws is ws else _raw_stream(x.get_device())
         self.cg = groups.c_struct()
+        self.ys = list(ys)
         # the tensors themselves: an adapter whose fields are set anew later does
         # not take the memory away that these arguments point to
-        self.x, self.keep = x, (groups, [(ad.a, ad.b, ad.scale) for ad in adapters], list(ys))
+        self.x, self.keep = x, (groups, [(ad.a, ad.b, ad.scale) for ad in adapters])
         self.args = (self.m, n, ctypes.byref(self.cg), _ptr(x), m, k, _xt(ys[0]), _ptr(self.ws), self.nws)
 
     def launch(self):
+        for y in self.ys:
+            if y.requires_grad and torch.is_grad_enabled():
+                raise ValueError("adapters are added in place, without a gradient: a y requires one")
         if self.made_on is not None and _raw_stream(self.x.get_device()) != self.made_on:
             # no one else knows of this use: once dropped, the workspace would go
             # to the next tensor of its own stream while the kernels still run
             self.ws.record_stream(torch.cuda.current_stream(self.x.device))
         _call("qg_lora_add", self.x, *self.args)
+        # a backward pass that has saved a y must see that it changed
+        torch.autograd.graph.increment_version(self.ys)
 
 
 def lora_add(x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters], ys: Sequence[torch.Tensor],
              ws: Optional[torch.Tensor] = None):
     """Adds the rows' low-rank adapters (qg_lora_add) to the projections' outputs
     ys [rows][n], in place: x bf16 [rows][k], groups = group_rows of the rows'
-    adapter numbers (rows without one are left as they were). Returns ys."""
+    adapter numbers (rows without one are left as they were). No gradient passes:
+    a y that requires one is refused while gradients are on. Returns ys."""
     LoraLaunch(x, groups, adapters, ys, ws).launch()
     return ys
 

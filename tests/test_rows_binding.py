@@ -87,3 +87,39 @@ def test_workspace_is_recorded_on_other_streams(qg, monkeypatch):
         given.launch()
     assert own.ws.streams == ["stream 9", "stream 8"] and given.ws.streams == []
     assert calls == ["qg_lora_add"] * 8
+
+
+def test_adds_in_place_are_seen_by_autograd(qg, monkeypatch):
+    """An output that a backward pass has saved: that pass fails, as after any
+    addition in place.  One that needs a gradient is refused, unless gradients
+    are off."""
+    monkeypatch.setattr(qg._binding, "_call", lambda name, x, *args: None)
+    x, ys = bf16(8, 256), [torch.zeros(8, 32), torch.zeros(8, 48)]
+    ads = [adapters(qg), adapters(qg, n=48)]
+    weight = torch.ones(48, requires_grad=True)
+    for y in ys:
+        loss = (y * weight[:y.shape[1]]).sum()
+        qg.lora_add(x, plan(qg), ads, ys)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    launch = qg.LoraLaunch(x, plan(qg), ads, ys)
+    ys[1].requires_grad_()
+    with pytest.raises(ValueError):
+        launch.launch()
+    with torch.no_grad():
+        before = ys[1]._version
+        launch.launch()
+    assert ys[1]._version == before + 1
+    with torch.inference_mode():  # tensors without versions
+        qg.lora_add(bf16(8, 256), plan(qg), ads[:1], [torch.zeros(8, 32)])
+
+
+def test_nothing_is_marked_as_written_by_a_refused_call(qg, monkeypatch):
+    def refuse(name, x, *args):
+        raise qg.QgError(2, name)
+
+    monkeypatch.setattr(qg._binding, "_call", refuse)
+    y = torch.zeros(8, 32)
+    with pytest.raises(qg.QgError):
+        qg.lora_add(bf16(8, 256), plan(qg), [adapters(qg)], [y])
+    assert y._version == 0
