@@ -873,10 +873,14 @@ class QExperts:
         per = (self.n + 15) // 16 * 16 if self.fmt == QG_WFMT_INT8_T16 else self.n
         if self.codes.numel() != self.e * per * self.k or self.scale.numel() != self.e * self.n:
             raise ValueError("codes or scale do not hold %d experts of [%d][%d]" % (self.e, self.n, self.k))
-        object.__setattr__(self, "_c", CExperts(self.fmt, 0, self.e, self.n, self.k, self.codes.data_ptr(),
-                                                   self.scale.data_ptr()))
+        at = (self.codes.data_ptr(), self.scale.data_ptr())
+        object.__setattr__(self, "_at", at)
+        object.__setattr__(self, "_c", CExperts(self.fmt, 0, self.e, self.n, self.k, *at))
 
     def c_struct(self) -> CExperts:
+        # weights whose data was set anew (a module moved) are not where they were
+        if (self.codes.data_ptr(), self.scale.data_ptr()) != self._at:
+            self.__post_init__()
         return self._c
 
 

@@ -123,3 +123,27 @@ def test_nothing_is_marked_as_written_by_a_refused_call(qg, monkeypatch):
     with pytest.raises(qg.QgError):
         qg.lora_add(bf16(8, 256), plan(qg), [adapters(qg)], [y])
     assert y._version == 0
+
+
+def test_experts_follow_their_tensors(qg):
+    """Codes and scales whose data is set anew (a module moved to another
+    device does that to its parameters): the products get the new memory,
+    checked, never the old."""
+    codes = torch.nn.Parameter(torch.zeros(2, 20, 128, dtype=torch.int8), requires_grad=False)
+    scale = torch.nn.Parameter(torch.ones(2, 20), requires_grad=False)
+    w = qg.QExperts(qg.QG_WFMT_INT8, 2, 20, 128, codes, scale)
+    for t in (codes, scale):
+        old = t.data
+        t.data = old.clone()
+        assert t.data_ptr() != old.data_ptr()
+        c = w.c_struct()
+        assert (c.codes, c.scale) == (codes.data_ptr(), scale.data_ptr())
+        assert (c.fmt, c.e, c.n, c.k) == (qg.QG_WFMT_INT8, 2, 20, 128)
+    for t, bad in ((codes, torch.zeros(2, 19, 128, dtype=torch.int8)), (codes, torch.zeros(2, 20, 128)),
+                   (scale, torch.ones(39)), (scale, torch.ones(2, 20, dtype=torch.float64))):
+        good = t.data
+        t.data = bad
+        with pytest.raises(ValueError):
+            w.c_struct()
+        t.data = good
+    assert w.c_struct().codes == codes.data_ptr()
