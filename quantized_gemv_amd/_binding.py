@@ -762,11 +762,18 @@ def _workspace(ws: Optional[torch.Tensor], need: int, like: torch.Tensor):
     return ws, ws.numel()
 
 
+def _memory(*tensors: Optional[torch.Tensor]):
+    """What keeps the tensors' memory where it is, also if their data is set
+    anew (a module that moves does that to its parameters)."""
+    return [t.untyped_storage() for t in tensors if t is not None]
+
+
 @dataclass(frozen=True)
 class RowGroups:
     """A row plan (qg_group_rows): the rows sorted by group. offsets
     [groups + 1], order and pos [rows], int32 on the device; per_row plan rows
-    read one row of x (a router's top_k).  Checked once, when it is made."""
+    read one row of x (a router's top_k).  Checked once, when it is made: calls
+    read and write the memory that the tensors have then."""
     offsets: torch.Tensor
     order: torch.Tensor
     pos: torch.Tensor
@@ -782,6 +789,7 @@ class RowGroups:
         put(self, "groups", self.offsets.numel() - 1)
         put(self, "rows", self.order.numel())
         put(self, "ptrs", (self.offsets.data_ptr(), self.order.data_ptr(), self.pos.data_ptr()))
+        put(self, "_keep", _memory(self.offsets, self.order, self.pos))
         put(self, "_c", tuple(CRowGroups(self.ptrs[0], order, self.rows, self.groups, self.per_row)
                               for order in (None, self.ptrs[1])))
 
@@ -804,6 +812,7 @@ class Routing:
         if self.ids.dim() != 2 or self.weights.shape != self.ids.shape or self.ids.numel() != self.groups.rows \
                 or self.ids.shape[1] != self.groups.per_row:
             raise ValueError("ids and weights must be [tokens][top_k], one per row of the plan")
+        object.__setattr__(self, "_keep", _memory(self.ids, self.weights))
         object.__setattr__(self, "ptrs", (self.ids.data_ptr(), self.weights.data_ptr()) + self.groups.ptrs)
 
 
@@ -985,7 +994,7 @@ def qgemm_experts_combine(w: QExperts, x: torch.Tensor, groups: RowGroups, weigh
     ws, nws = _workspace(ws, int(lib().qg_experts_combine_workspace_bytes(groups.rows, w.n)), x)
     cg = groups.c_struct(gather)
     _call("qg_qgemm_experts_combine", x, ctypes.byref(w.c_struct()), ctypes.byref(cg), amode, _ptr(x), _ptr(s_x), x.shape[0],
-          _ptr(groups.pos), _ptr(weights), tokens, _ptr(y), _xt(y), _ptr(ws), nws)
+          groups.ptrs[2], _ptr(weights), tokens, _ptr(y), _xt(y), _ptr(ws), nws)
     return y
 
 
@@ -1067,9 +1076,10 @@ class LoraLaunch:
         self.made_on = None if self.ws is ws else _raw_stream(x.get_device())
         self.cg = groups.c_struct()
         self.ys = list(ys)
-        # the tensors themselves: an adapter whose fields are set anew later does
-        # not take the memory away that these arguments point to
-        self.x, self.keep = x, (groups, [(ad.a, ad.b, ad.scale) for ad in adapters])
+        # the memory itself: adapters whose fields, or tensors whose data, are set
+        # anew later do not take it away from these arguments
+        self.x = x.detach()
+        self.keep = (groups, _memory(x, self.ws, *ys, *(t for ad in adapters for t in (ad.a, ad.b, ad.scale))))
         self.args = (self.m, n, ctypes.byref(self.cg), _ptr(x), m, k, _xt(ys[0]), _ptr(self.ws), self.nws)
 
     def launch(self):

@@ -1,5 +1,9 @@
 """The binding of the row-dependent products on the CPU: what its objects check
 and keep.  Host tensors stand in for device tensors; nothing is launched."""
+import gc
+import weakref
+
+import numpy as np
 import pytest
 import torch
 
@@ -147,3 +151,49 @@ def test_experts_follow_their_tensors(qg):
             w.c_struct()
         t.data = good
     assert w.c_struct().codes == codes.data_ptr()
+
+
+def watched(dtype, *shape):
+    """A zero tensor over memory of numpy's, and a reference that dies with that
+    memory."""
+    host = np.zeros(shape + (torch.empty((), dtype=dtype).element_size(),), np.uint8)
+    t = torch.empty(0, dtype=dtype)
+    t.set_(torch.from_numpy(host).untyped_storage(), 0, shape)
+    return t, weakref.ref(host)
+
+
+def replaced(tensors):
+    """Their data set anew, as a module that moves does to its parameters."""
+    for t in tensors:
+        t.data = torch.ones(3, dtype=t.dtype)
+    gc.collect()
+
+
+def test_a_plan_keeps_the_memory_it_points_to(qg):
+    i32 = torch.int32
+    tensors, alive = zip(*(watched(i32, n) for n in (5, 8, 8)))
+    more, more_alive = zip(watched(i32, 4, 2), watched(torch.float32, 4, 2))
+    r = qg.Routing(more[0], more[1], qg.RowGroups(*tensors, 2))
+    at = r.ptrs
+    replaced(tensors + more)
+    assert all(a() is not None for a in alive + more_alive) and r.ptrs == at
+    assert [a().ctypes.data for a in more_alive + alive] == list(at)
+    assert r.groups.c_struct().order == at[3] and r.groups.c_struct().offsets == at[2]
+    del r
+    gc.collect()
+    assert not any(a() is not None for a in alive + more_alive)
+
+
+def test_a_launch_keeps_the_memory_it_points_to(qg):
+    bf = torch.bfloat16
+    shapes = [(bf, 8, 256), (bf, 4, 16, 256), (bf, 4, 32, 16), (torch.float32, 4), (torch.float32, 8, 32)]
+    (x, a, b, scale, y), alive = zip(*(watched(*s) for s in shapes))
+    groups = plan(qg)
+    launch = qg.LoraLaunch(x, groups, [qg.LoraAdapters(a, b, scale)], [y])
+    replaced((x, a, b, scale, y))
+    assert all(r() is not None for r in alive)
+    m = launch.m[0]
+    assert [r().ctypes.data for r in alive] == [launch.args[3], m.a, m.b, m.scale, m.y]
+    del launch
+    gc.collect()
+    assert not any(r() is not None for r in alive)
