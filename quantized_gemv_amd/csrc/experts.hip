@@ -56,7 +56,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + e
 template <int YT>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
     if constexpr (YT == 0) static_cast<float*>(y)[at] = v;
-    else static_cast<uint16_t*>(y)[at] = (uint16_t)f32_to_bf16(v);
+    else static_cast<uint16_t*>(y)[at] = (uint16_t)any_f32_to_bf16(v);
 }
 
 // ------------------------------------------------------------------ streams
@@ -454,7 +454,7 @@ __device__ __forceinline__ void experts_tile(const ExpertParams& p, const RowTil
 #pragma unroll
             for (int b = 0; b < (GLU ? 1 : 2); ++b) {
                 if constexpr (YT == 0) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[b]), ry, yoff[b] + row * line, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16(o[b]), ry, yoff[b] + row * line, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)any_f32_to_bf16(o[b]), ry, yoff[b] + row * line, 0, 0);
             }
         }
     }
@@ -628,7 +628,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineParams p) {
             *reinterpret_cast<c4f*>(static_cast<float*>(a.y) + out) = s;
         } else {
             *reinterpret_cast<c4h*>(static_cast<uint16_t*>(a.y) + out) =
-                c4h{f32_to_bf16(s[0]) | (f32_to_bf16(s[1]) << 16), f32_to_bf16(s[2]) | (f32_to_bf16(s[3]) << 16)};
+                c4h{any_f32_to_bf16(s[0]) | (any_f32_to_bf16(s[1]) << 16), any_f32_to_bf16(s[2]) | (any_f32_to_bf16(s[3]) << 16)};
         }
     } else {
 #pragma unroll

@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
                     const y_t o = {v[0], v[1], v[2], v[3]};
                     write_y<MT != 1>(o, reinterpret_cast<y_t*>(static_cast<float*>(m.y) + yat[s] + at));
                 } else {
-                    const y_t o = {f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16), f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16)};
+                    const y_t o = {any_f32_to_bf16(v[0]) | (any_f32_to_bf16(v[1]) << 16), any_f32_to_bf16(v[2]) | (any_f32_to_bf16(v[3]) << 16)};
                     write_y<MT != 1>(o, reinterpret_cast<y_t*>(static_cast<uint16_t*>(m.y) + yat[s] + at));
                 }
             } else {
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
                 for (int e = 1; e < 4; ++e) {
                     if (e >= skip) {
                         if constexpr (YT == 0) static_cast<float*>(m.y)[yat[s] + at + e] = v[e];
-                        else static_cast<uint16_t*>(m.y)[yat[s] + at + e] = (uint16_t)f32_to_bf16(v[e]);
+                        else static_cast<uint16_t*>(m.y)[yat[s] + at + e] = (uint16_t)any_f32_to_bf16(v[e]);
                     }
                 }
             }
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float f = v[e] * scale;
-            term[0][e] = f32_to_bf16(f);
+            term[0][e] = any_f32_to_bf16(f);  // NaN here is enough for the sum
             const float f1 = f - bf16_to_f32(term[0][e]);
             term[1][e] = f32_to_bf16(f1);
             term[2][e] = f32_to_bf16(f1 - bf16_to_f32(term[1][e]));

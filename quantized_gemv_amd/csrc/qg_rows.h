@@ -12,6 +12,11 @@
 
 namespace qg {
 
+// Round-to-nearest-even narrowing of any fp32 to bf16 bits.  NaN stays NaN:
+// the rounding sum of f32_to_bf16 would carry payloads from 0x7FFF8000 on over
+// into a zero, and scales and weights come from outside with any payload.
+__device__ __forceinline__ uint32_t any_f32_to_bf16(float f) { return f != f ? 0x7FC0u : f32_to_bf16(f); }
+
 // Inclusive prefix sum over the wave (all 64 lanes active): DPP row shifts
 // within the rows of 16, then the row totals carried up.
 template <int CTRL, int ROW_MASK>

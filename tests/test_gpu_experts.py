@@ -222,6 +222,30 @@ def test_non_finite_rows_stay_alone(qg):
         assert np.array_equal(y0[~rows], y1[~rows]) and not np.isfinite(y1[c.order == 3]).any()
 
 
+# fp32 NaN whose upper half a rounding by adding to the bits carries over into
+# a zero of either sign
+NANS = np.array([0x7FFFFFFF, 0xFFFFFFFF, 0x7FFF8000, 0x7FC00000], np.uint32).view(np.float32)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("act8", [False, True])
+def test_nan_scales_and_weights_reach_y(qg, act8, bf16):
+    note("NaN of every payload in scales and weights, act8=%s bf16=%s" % (act8, bf16))
+    dt = torch.bfloat16 if bf16 else torch.float32
+    for t, e, n in ((16, 2, 96), (600, 2, 520)):  # streams, tiles
+        c = Case(qg, t, e, 1, 256, n, act8, True, 8, mats=2, gather=True)
+        c.scale[0][:, 5:9] = NANS
+        c.w[0].scale.copy_(dev(c.scale[0]))
+        for y in (qg.qgemm_experts(c.w[0], c.xd, c.groups, s_x=c.sxd, y_dtype=dt),
+                  qg.qgemm_experts_swiglu(c.w[0], c.w[1], c.xd, c.groups, s_x=c.sxd, y_dtype=dt)):
+            odd = torch.isnan(y).cpu().numpy()
+            assert odd[:, 5:9].all() and not odd[:, :5].any() and not odd[:, 9:].any()
+        c.weights[3:7, 0] = NANS
+        y = qg.qgemm_experts_combine(c.w[1], c.xd, c.groups, dev(c.weights), s_x=c.sxd, gather=True, y_dtype=dt)
+        odd = torch.isnan(y).cpu().numpy()
+        assert odd[3:7].all() and not odd[:3].any() and not odd[7:].any()
+
+
 def test_long_k(qg):
     note("experts with the largest k of each mode")
     for k, act8 in ((qg.QG_BATCH_MAX_K, False), (qg.QG_QGEMM_MAX_K, True)):

@@ -258,6 +258,20 @@ def test_values_that_are_not_finite_stay_in_their_rows(qg):
     assert np.all(np.abs(got[~odd] - want[~odd]) <= tol[~odd])
 
 
+@pytest.mark.parametrize("ybf16", [False, True])
+def test_nan_scales_reach_y(qg, ybf16):
+    """Also those whose upper half a rounding by adding to the bits carries
+    over into a zero."""
+    note("NaN of every payload in the adapters' scales, ybf16=%s" % ybf16)
+    nans = np.array([0x7FFFFFFF, 0xFFFFFFFF, 0x7FFF8000, 0x7FC00000], np.uint32).view(np.float32)
+    for m in (40, 600):
+        c = Case(qg, m, 6, 256, [(24, 70)], ybf16, 20, drop=0.2)
+        c.ad[0].scale[1:5] = dev(nans)
+        qg.lora_add(c.xd, c.groups, c.ad, c.ys)
+        assert np.array_equal(np.isnan(bf16_to_f64(host(c.ys[0])) if ybf16 else host(c.ys[0])),
+                              np.repeat(((c.ids >= 1) & (c.ids < 5))[:, None], 70, axis=1))
+
+
 def test_refusals(qg):
     c = Case(qg, 8, 4, 256, [(16, 32)], False, 1)
     x, gr, ad, ys = c.xd, c.groups, c.ad, c.ys
