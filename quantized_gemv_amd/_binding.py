@@ -1078,21 +1078,23 @@ class LoraLaunch:
         self.ys = list(ys)
         # the memory itself: adapters whose fields, or tensors whose data, are set
         # anew later do not take it away from these arguments
-        self.x = x.detach()
+        self.x, self.index = x.detach(), x.get_device()
         self.keep = (groups, _memory(x, self.ws, *ys, *(t for ad in adapters for t in (ad.a, ad.b, ad.scale))))
-        self.args = (self.m, n, ctypes.byref(self.cg), _ptr(x), m, k, _xt(ys[0]), _ptr(self.ws), self.nws)
+        # as C values: converted once, not by every launch
+        self.args = (ctypes.cast(self.m, ctypes.POINTER(CLora)), _c_i32(n), ctypes.pointer(self.cg), _c_vp(x.data_ptr()),
+                     _c_i64(m), _c_i64(k), _c_i32(_xt(ys[0])), _c_vp(_ptr(self.ws)), _c_sz(self.nws))
 
     def launch(self):
         for y in self.ys:
             if y.requires_grad and torch.is_grad_enabled():
                 raise ValueError("adapters are added in place, without a gradient: a y requires one")
-        if self.made_on is not None and _raw_stream(self.x.get_device()) != self.made_on:
+        if self.made_on is not None and _raw_stream(self.index) != self.made_on:
             # no one else knows of this use: once dropped, the workspace would go
             # to the next tensor of its own stream while the kernels still run
             self.ws.record_stream(torch.cuda.current_stream(self.x.device))
         _call("qg_lora_add", self.x, *self.args)
         # a backward pass that has saved a y must see that it changed
-        torch.autograd.graph.increment_version(self.ys)
+        torch._C._increment_version(self.ys)
 
 
 def lora_add(x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters], ys: Sequence[torch.Tensor],

@@ -193,7 +193,7 @@ def test_a_launch_keeps_the_memory_it_points_to(qg):
     replaced((x, a, b, scale, y))
     assert all(r() is not None for r in alive)
     m = launch.m[0]
-    assert [r().ctypes.data for r in alive] == [launch.args[3], m.a, m.b, m.scale, m.y]
+    assert [r().ctypes.data for r in alive] == [launch.args[3].value, m.a, m.b, m.scale, m.y]
     del launch
     gc.collect()
     assert not any(r() is not None for r in alive)
