@@ -297,6 +297,74 @@ def test_x_past_4_gib(qg):
     assert not y[rest].any()
 
 
+@pytest.mark.parametrize("n", [32, 600])  # 32-row and 128-row tiles
+@pytest.mark.parametrize("act8", [False, True])
+def test_tiles_read_x_just_below_4_gib(qg, act8, n):
+    note("tiles over an x of almost 4 GiB, act8=%s n=%d" % (act8, n))
+    k, rows, e = 131072, 32000 if act8 else 16000, 2
+    x = torch.zeros((rows, k), dtype=torch.int8 if act8 else torch.bfloat16, device="cuda")
+    g = synth.rng(13)
+    at = np.array([0, rows // 4, rows // 2 - 1, rows // 2, 3 * rows // 4, rows - 2, rows - 1])
+    if act8:
+        vals = g.integers(-127, 128, (len(at), k)).astype(np.int8)
+        x[torch.from_numpy(at).cuda()] = dev(vals)
+    else:
+        bits = synth.to_bf16_bits(synth.gaussian(g, (len(at), k), 1.0))
+        vals = synth.bf16_bits_to_f32(bits)
+        x[torch.from_numpy(at).cuda()] = dev_bf16(bits)
+    codes = g.integers(-127, 128, (e, n, k)).astype(np.int8)
+    w = qg.QExperts(qg.QG_WFMT_INT8, e, n, k, dev(codes), torch.full((e, n), 30000.0, device="cuda"))
+    ids = g.integers(0, e, rows).astype(np.int32)
+    plan = qg.group_rows(dev(ids), e)
+    y = qg.qgemm_experts(w, x, plan, s_x=torch.ones(rows, device="cuda") if act8 else None)
+    pos = host(plan.pos)
+    got = host(y[torch.from_numpy(pos[at].astype(np.int64)).cuda()])
+    for j, r in enumerate(at):
+        want = vals[j].astype(np.float64) @ codes[ids[r]].astype(np.float64).T / 30000.0
+        tol = 8 * HALF * np.abs(want) if act8 else TOL_F32 * np.abs(want).max()
+        assert np.all(np.abs(got[j] - want) <= tol), "row %d" % r
+    assert int((y != 0).any(1).sum()) == len(at)
+
+
+def test_outputs_past_4_gib(qg):
+    note("tiles and combine whose products pass 4 GiB")
+    t, top, e, k, n = 20000, 2, 4, 128, 32768
+    g = synth.rng(14)
+    bits = synth.to_bf16_bits(synth.gaussian(g, (t, k), 1.0))
+    x = synth.bf16_bits_to_f32(bits).astype(np.float64)
+    codes = g.integers(-127, 128, (e, n, k)).astype(np.int8)
+    w = qg.QExperts(qg.QG_WFMT_INT8, e, n, k, dev(codes), torch.full((e, n), 800.0, device="cuda"))
+    ids = np.stack([g.permutation(e)[:top] for _ in range(t)]).astype(np.int32)
+    wt = g.random((t, top)).astype(np.float32)
+    plan = qg.group_rows(dev(ids), e)
+    y = qg.qgemm_experts(w, dev_bf16(bits), plan)
+    out = qg.qgemm_experts_combine(w, dev_bf16(bits), plan, dev(wt), gather=True)
+    pos = host(plan.pos).reshape(t, top)
+    for r in (0, 1, t // 2, t - 2, t - 1, int(np.argmax(pos.max(1)))):
+        rows = [x[r] @ codes[ids[r, j]].astype(np.float64).T / 800.0 for j in range(top)]
+        for j in range(top):
+            assert np.abs(host(y[int(pos[r, j])]) - rows[j]).max() <= TOL_F32 * np.abs(rows[j]).max()
+        want = wt[r].astype(np.float64) @ np.array(rows)
+        tol = wt[r].astype(np.float64) @ np.array([TOL_F32 * np.abs(v).max() + top * HALF * np.abs(v) for v in rows])
+        assert np.all(np.abs(host(out[r]) - want) <= tol)
+
+
+@pytest.mark.parametrize("t", [5, 400])
+def test_the_same_expert_twice(qg, t):
+    """A choice that names an expert twice for a token (another router's) adds
+    both of its products."""
+    note("the same expert in two slots, t=%d" % t)
+    c = Case(qg, t, 4, 3, 256, 130, False, True, 17)
+    ids = synth.rng(18).integers(0, 4, (t, 3)).astype(np.int32)
+    ids[:, 1] = ids[:, 0]
+    c.offsets, c.order, c.pos = R.group_rows(ids, 4)
+    c.live = int(c.offsets[-1])
+    c.groups = qg.group_rows(dev(ids), 4)
+    full, y = out_buffer(t, 130, False)
+    qg.qgemm_experts_combine(c.w[0], c.xd, c.groups, dev(c.weights), gather=True, y=y)
+    check(full, y, t, *c.combine(), False)
+
+
 def test_very_wide_matrix(qg):
     note("a matrix of more than 2^21 rows")
     n, k, t = 2100003, 128, 200

@@ -126,6 +126,22 @@ def test_lora_long_k(qg):
         c.check()
 
 
+@pytest.mark.parametrize("m,groups,used,mats", [
+    (1000, 256, 12, [(64, 300), (16, 64)]),  # a prompt of a few requests, many adapters loaded
+    (1000, 1024, 1, [(16, 200)]),
+    (70, 1024, 2, [(128, 130)]),
+])
+def test_lora_few_of_many_adapters(qg, m, groups, used, mats):
+    note("lora m=%d, %d of %d adapters in use" % (m, used, groups))
+    c = Case(qg, m, groups, 256, mats, False, 8, drop=0.1, runs=True)
+    g = synth.rng(9)
+    of = g.choice(groups, size=used, replace=False)
+    c.ids = np.where(c.ids < 0, -1, np.sort(of[g.integers(0, used, m)])).astype(np.int32)
+    c.groups = qg.group_rows(dev(c.ids), groups)
+    qg.lora_add(c.xd, c.groups, c.ad, c.ys)
+    c.check()
+
+
 def test_lora_repeats_bit_for_bit(qg):
     note("lora twice on the same inputs")
     c = Case(qg, 90, 5, 1024, [(32, 200)], False, 7, runs=True)

@@ -67,6 +67,33 @@ def test_group_rows(qg, rows, groups, drop):
     check_plan(qg.group_rows(dev(ids), groups), *want)
 
 
+def test_group_rows_most(qg):
+    """The longest plan there can be, checked on the device: places and rows
+    are each other's inverse, sorted by id, equal ids in row order."""
+    rows, groups = qg.QG_MAX_PLAN_ROWS, 1000
+    note("group_rows of %d rows" % rows)
+    ids = torch.randint(-3, groups + 3, (rows,), dtype=torch.int32, device="cuda",
+                        generator=torch.Generator(device="cuda").manual_seed(4))
+    plan = qg.group_rows(ids, groups)
+    count = torch.zeros(groups, dtype=torch.int64, device="cuda")
+    piece = 1 << 27
+    for lo in range(0, rows, piece):
+        part = ids[lo:lo + piece]
+        inside = (part >= 0) & (part < groups)
+        count += torch.bincount(part[inside], minlength=groups)
+        pos = plan.pos[lo:lo + piece]
+        assert torch.equal(pos >= 0, inside)
+        back = plan.order[pos.clamp(min=0).long()]
+        assert bool((back == torch.arange(lo, lo + part.numel(), dtype=torch.int32, device="cuda"))[inside].all())
+    assert torch.equal(plan.offsets[1:].long(), torch.cumsum(count, 0)) and int(plan.offsets[0]) == 0
+    live = int(plan.offsets[-1])
+    assert bool((plan.order[live:] == -1).all())
+    for lo in range(0, live - 1, piece):
+        order = plan.order[lo:min(lo + piece + 1, live)]
+        of = ids[order.long()]
+        assert bool(((of[1:] > of[:-1]) | ((of[1:] == of[:-1]) & (order[1:] > order[:-1]))).all())
+
+
 def test_group_rows_one_group_holds_all_and_none(qg):
     note("group_rows all equal / all dropped")
     for v in (3, -1):
