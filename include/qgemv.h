@@ -762,7 +762,8 @@ qg_status qg_group_rows(const int32_t* ids, int64_t rows, int32_t groups, int32_
  *          p = t * top_k + j (out).
  * 1 <= top_k <= min(experts, QG_MAX_TOP_K); experts <= QG_MAX_ROW_GROUPS;
  * tokens * top_k <= QG_MAX_PLAN_ROWS.  ws as qg_group_rows of
- * (tokens * top_k, experts).
+ * (tokens * top_k, experts).  Outputs must not overlap logits, one another or
+ * ws.
  */
 qg_status qg_moe_route(const void* logits, int32_t xt, int64_t tokens, int32_t experts, int32_t top_k,
                        int32_t renorm, int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* pos,
@@ -820,6 +821,9 @@ typedef struct qg_experts {
  * rows * n <= 2^40; 1 <= x_rows < 2^31, and x_rows >= rows where order is
  * NULL; per_row in [1, QG_MAX_TOP_K].  codes, x and y 16-B aligned; the other
  * arrays aligned to their elements.  Outputs must not overlap inputs.
+ * With many rows per expert, an x of 4 GiB or more, or n of 2^21 or more, takes
+ * 6 to 8 times as long per row as one below (kernels for few rows run): such
+ * products are better called in parts.
  */
 qg_status qg_qgemm_experts(const qg_experts* w, const qg_row_groups* groups, int32_t amode, const void* x,
                            const float* s_x, int64_t x_rows, void* y, int32_t yt, void* stream);
@@ -847,7 +851,9 @@ qg_status qg_qgemm_experts_combine(const qg_experts* w, const qg_row_groups* gro
  * groups <= QG_MAX_ROW_GROUPS; x_rows * k, x_rows * n, groups * n * r and
  * groups * r * k <= 2^40.  a, b, x, y 16-B aligned; two y that share bytes are
  * QG_ERR_ARG.  Values that are not finite, in x, A, B or scale A x rounded to
- * bf16, reach the outputs that they enter as NaN.
+ * bf16, reach the outputs that they enter as NaN.  No y may overlap b, scale,
+ * the plan or ws.  Tile heights and parts go by rows per group, as if every
+ * group had some: a plan and matrices of the adapters in use only run faster.
  * ws: qg_lora_workspace_bytes(...) bytes for the same m (its r), count,
  *     rows, groups and k, 16-B aligned; contents on entry do not matter.
  *     Calls that overlap on one workspace race.

@@ -74,7 +74,8 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 // HBM bounds it.  Small workgroups with little in registers keep the most of
 // them on a CU, so that one's start (tile search, row numbers) and end hide
 // behind the others' loads.  Waves per workgroup x tiles per wave x units per
-// step, us of the four cases with few rows (180, 237, 119 and 94 MB of codes):
+// step, us of four calls with few rows (180, 199, 100 and 88 MB of codes of the
+// chosen experts):
 // 4 x 2 x 1: 32.5, 32.8, 24.6, 25.0; 4 x 4 x 2: 34.1, 36.3, 26.1, 25.0;
 // 8 x 4 x 2: 35.7, 45.0, 30.9, 29.2; 2 x 2 x 1: 33.9, 33.0, 25.0, 26.1.
 // Row-major codes, two loads of 16 bytes per lane that read whole 128-byte
@@ -530,19 +531,31 @@ static hipError_t run_tile(ExpertParams p, hipStream_t st) {
 template <int ACT, int YT, bool GLU>
 static hipError_t run_kind(const ExpertParams& p, hipStream_t st) {
     // Streams up to nine rows per expert, tiles above.  Measured, us, stream and
-    // 128-row tiles (swiglu, tiled codes, bf16 x): 64 experts of 1024 x 2048 at
-    // 4, 8, 12, 24 rows each 39 46, 50 54, 62 55, 98 61; 8 of 4096 x 4096: 46 52,
-    // 49 52, 62 54, 99 55.  Where 128-row tiles do not fill the CUs, a
-    // workgroup's own time decides: 32-row tiles then, or streams while all of
-    // them together read few matrix rows.  Stream, 32-row, 128-row tiles
-    // (products): 5 of 440 x 2176 at 64, 256, 1024 rows 13 17 30, 22 18 34, 71 27
-    // 36; 16 of 1024 x 2048 at 16, 32, 128 rows 14 17 19, 20 17 25, 53 25 34; at
-    // 256 tiles of 128 rows and above the two tiles are even (32 of 704 x 1024,
-    // 256 rows: 26 23), and with more of them 128 rows win.
+    // 128-row tiles of a swiglu at 8, 12, 24 rows per expert:
+    //                          64 of 1024 x 2048        16 of 2304 x 4096
+    //   bf16 x, tiled codes    47 50, 58 51, 95 57      56 60, 69 62, 109 69
+    //   bf16 x, row-major      57 58, 72 59, 114 63     67 98, 83 100, 132 106
+    //   int8 x, tiled codes    44 47, 53 48, 84 52      53 66, 63 67, 96 70
+    //   int8 x, row-major      48 51, 58 53, 93 57      55 91, 66 91, 104 95
+    // (row-major codes of few wide experts would stay streams up to 16 rows: 97
+    // 102 and 77 93.)  Where 128-row tiles do not fill the CUs, a workgroup's own
+    // time decides: 32-row tiles then, or streams while all of them together read
+    // few matrix rows.  Stream, 32-row, 128-row tiles (products) of 5 experts of
+    // 440 x 2176 at 64, 256, 1024 rows each, and of 16 of 1024 x 2048 at 32, 128:
+    //   bf16 x, tiled codes    12 17 32, 21 17 32, 68 30 35    19 17 28, 52 24 32
+    //   bf16 x, row-major      13 21 32, 26 21 32, 80 38 33    24 21 28, 69 36 31
+    //   int8 x, tiled codes    11 10 18, 18 11 19, 54 17 19    16 11 16, 42 17 19
+    //   int8 x, row-major      11 19 23, 20 20 24, 62 36 25    19 20 22, 54 36 24
+    // (the codes' layout is not asked: row-major ones would take 128-row tiles from
+    // about 100 rows per expert on, at 256 rows of the second 51 and 25 with int8
+    // x).  At 256 tiles of 128 rows and above the two tiles are even with tiled
+    // codes (32 of 704 x 1024, 256 rows: 25 22), and with more of them 128 rows win.
     constexpr int kPer = GLU ? kTN / 2 : kTN;
     const bool fills = max_row_tiles(p.rows, p.e, 128) * ((p.n + kPer - 1) / kPer) >= 256;
     const int64_t streamed = max_row_tiles(p.rows, p.e, 16) * p.n * (GLU ? 2 : 1);
-    // the tile kernel keeps 32-bit offsets into x and a tile's y
+    // The tile kernel keeps 32-bit offsets into x and a tile's y; past them many
+    // rows cost several times as much (8 experts of 1024 x 8192, bf16 x: 262016
+    // rows 3.6 ms in tiles, 262144 rows 23.2 ms in streams).
     const bool small = (int64_t)p.x_rows * p.k * (ACT == 0 ? 2 : 1) < ((int64_t)1 << 32) && p.n < (1 << 21);
     if (p.rows <= 9 * (int64_t)p.e || (!fills && streamed < 28000) || !small)
         return p.tiled ? run_stream<ACT, YT, GLU, true>(p, st) : run_stream<ACT, YT, GLU, false>(p, st);

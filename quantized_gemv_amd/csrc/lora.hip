@@ -13,8 +13,9 @@
 // runs on the same matrix instructions; y is read, added to and written once.
 //
 // Few rows: the latency of two dependent launches (16 rows, rank 16, 4096 x
-// 4096: 4.2 + 4.4 us).  Many: reading and writing y (4129 rows of 11008 fp32,
-// rank 64: 72 us for 364 MB, 5.1 TB/s, after 17 us of shrink).
+// 4096: 4.2 + 4.4 us).  Many: reading and writing y (4129 rows of 11008 fp32, a
+// tenth of them without an adapter, rank 64: 72 us for 327 MB, 4.5 TB/s, after
+// 17 us of shrink).
 #include "qg_launch.h"
 #include "qg_rows.h"
 
@@ -345,7 +346,10 @@ __global__ __launch_bounds__(kXThreads, MT == 1 ? 4 : 3) void lora_expand_kernel
     }
 }
 
-// 32 rows per workgroup where the groups have that many.
+// 32 rows per workgroup where the groups have that many.  The host knows the
+// groups there are, not those in use: 4096 rows of 12 adapters, rank 64, 4096 x
+// 11008, take 147 us with 256 loaded (119 with 32 rows) and 105 with those 12; of
+// rank 16, 4096 x 4096, with 1024 loaded 66 (32 rows: 82) and 43.
 static bool tall_groups(int64_t rows, int64_t groups) { return rows >= 32 * groups; }
 static int shrink_rows(int64_t rows, int64_t groups) { return tall_groups(rows, groups) ? 32 : 16; }
 
@@ -371,8 +375,10 @@ template <int YT, int MT, int KC, int CT>
 static hipError_t run_expand(LoraParams& p, int64_t widest, hipStream_t st) {
     const int64_t blocks = (widest + 64 * CT - 1) / (64 * CT), tiles = max_row_tiles(p.rows, p.groups, 16 * MT) * p.count;
     // Strips as long as they can be with enough workgroups left (us with the
-    // shrink; 4129 rows of 11008 fp32, rank 64: 1024, 2048, 4096, 8192 workgroups
-    // 106, 103, 98, 107; q, k, v of 61 rows: 512, 1024, 2048 20.1, 17.7, 19.5).
+    // shrink, at 512, 1024, 2048, 4096, 8192 workgroups.  16 rows: 48 rows of 11008,
+    // rank 16, 11.5 9.9 10.7 10.1 10.5; three of 500 x 4096, rank 32, 29 26 24 25 25;
+    // 32 rows: three of 4096 x 4096, rank 16, 132 112 110 101 101; 1500 x 14336, rank
+    // 32, 51 49 43 46 46; two of 2048 x 2048, rank 128, 50 51 53 53 53).
     int64_t per = blocks * tiles / (MT == 1 ? 1024 : 4096);
     per = per < 1 ? 1 : per > blocks ? blocks : per;
     p.strip_blocks = (int32_t)per;
