@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 from typing import Optional, Sequence
 
 import torch
@@ -768,8 +768,16 @@ def _memory(*tensors: Optional[torch.Tensor]):
     return [t.untyped_storage() for t in tensors if t is not None]
 
 
+class _FromFields:
+    """Copied, saved and loaded by its fields: the addresses that an object
+    holds are those of its own tensors."""
+
+    def __reduce__(self):
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
+
+
 @dataclass(frozen=True)
-class RowGroups:
+class RowGroups(_FromFields):
     """A row plan (qg_group_rows): the rows sorted by group. offsets
     [groups + 1], order and pos [rows], int32 on the device; per_row plan rows
     read one row of x (a router's top_k).  Checked once, when it is made: calls
@@ -798,7 +806,7 @@ class RowGroups:
 
 
 @dataclass(frozen=True)
-class Routing:
+class Routing(_FromFields):
     """What moe_route returns: ids and weights [tokens][top_k] and the plan.
     Checked once, when it is made."""
     ids: torch.Tensor
@@ -864,7 +872,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renorm: bool = True, out: Option
 
 
 @dataclass(frozen=True)
-class QExperts:
+class QExperts(_FromFields):
     """The experts' int8 matrices (qg_experts): codes [e][n][k] (QG_WFMT_INT8)
     or each expert's 16-row tiles (QG_WFMT_INT8_T16, tiled16_experts), scale
     [e][n]."""
@@ -1062,7 +1070,7 @@ class LoraLaunch:
         m, k = x.shape
         for ad, y in zip(adapters, ys):
             _dev(y, "y", (torch.float32, torch.bfloat16))
-            ad.check()  # its fields may have been set anew
+            LoraAdapters.check(ad)  # its fields may have been set anew
             _same_device(x, ad.a, y)
             if ad.a.shape[0] != groups.groups or ad.a.shape[2] != k:
                 raise ValueError("a must be [%d][r][%d]" % (groups.groups, k))

@@ -1,6 +1,8 @@
 """The binding of the row-dependent products on the CPU: what its objects check
 and keep.  Host tensors stand in for device tensors; nothing is launched."""
+import copy
 import gc
+import io
 import weakref
 
 import numpy as np
@@ -197,3 +199,26 @@ def test_a_launch_keeps_the_memory_it_points_to(qg):
     del launch
     gc.collect()
     assert not any(r() is not None for r in alive)
+
+
+@pytest.mark.parametrize("again", [copy.deepcopy, copy.copy, "saved"])
+def test_copies_point_to_their_own_memory(qg, again):
+    """Experts, plans and routings that are copied, or saved and loaded."""
+    def saved(v):
+        f = io.BytesIO()
+        torch.save(v, f)
+        return torch.load(io.BytesIO(f.getvalue()), weights_only=False)  # what this test has written
+
+    i32 = dict(dtype=torch.int32)
+    w = qg.QExperts(qg.QG_WFMT_INT8, 2, 20, 128, torch.ones(2, 20, 128, dtype=torch.int8), torch.ones(2, 20))
+    r = qg.Routing(torch.zeros(4, 2, **i32), torch.zeros(4, 2), qg.RowGroups(torch.zeros(5, **i32), torch.zeros(8, **i32),
+                                                                           torch.zeros(8, **i32), 2))
+    w2, r2 = (saved if again == "saved" else again)((w, r)) if again is not copy.copy else (copy.copy(w), copy.copy(r))
+    c = w2.c_struct()
+    assert (c.codes, c.scale) == (w2.codes.data_ptr(), w2.scale.data_ptr())
+    assert (c.fmt, c.e, c.n, c.k) == (qg.QG_WFMT_INT8, 2, 20, 128)
+    p = r2.groups
+    assert r2.ptrs == tuple(t.data_ptr() for t in (r2.ids, r2.weights, p.offsets, p.order, p.pos))
+    assert p.c_struct().order == p.order.data_ptr() and (p.rows, p.groups, p.per_row) == (8, 4, 2)
+    if again is not copy.copy:
+        assert c.codes != w.codes.data_ptr() and r2.ptrs[0] != r.ptrs[0]
