@@ -12,10 +12,14 @@
 
 namespace qg {
 
-// Round-to-nearest-even narrowing of any fp32 to bf16 bits.  NaN stays NaN:
-// the rounding sum of f32_to_bf16 would carry payloads from 0x7FFF8000 on over
-// into a zero, and scales and weights come from outside with any payload.
-__device__ __forceinline__ uint32_t any_f32_to_bf16(float f) { return f != f ? 0x7FC0u : f32_to_bf16(f); }
+// Round-to-nearest-even narrowing of any fp32 to bf16 bits, by the hardware's
+// conversion: the bits of f32_to_bf16 on every finite and infinite value (all
+// compared), and NaN stays NaN.  (The rounding sum of f32_to_bf16 would carry
+// payloads from 0x7FFF8000 on over into a zero, and scales and weights come from
+// outside with any payload.)
+__device__ __forceinline__ uint32_t any_f32_to_bf16(float f) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
 
 // Inclusive prefix sum over the wave (all 64 lanes active): DPP row shifts
 // within the rows of 16, then the row totals carried up.

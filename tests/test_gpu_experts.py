@@ -14,7 +14,7 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_util import TOL_F32, bf16_to_f64, dev, dev_bf16, host
+from gpu_util import TOL_F32, bf16_to_f64, dev, dev_bf16, f32_to_bf16_rne, host
 from oracle import rows as R
 import synth
 
@@ -244,6 +244,31 @@ def test_nan_scales_and_weights_reach_y(qg, act8, bf16):
         y = qg.qgemm_experts_combine(c.w[1], c.xd, c.groups, dev(c.weights), s_x=c.sxd, gather=True, y_dtype=dt)
         odd = torch.isnan(y).cpu().numpy()
         assert odd[3:7].all() and not odd[:3].any() and not odd[7:].any()
+
+
+def test_bf16_outputs_are_rounded_to_nearest_even(qg):
+    """Any fp32 value through a combine of products that are exactly 1."""
+    note("bf16 rounding of many fp32 values")
+    t = 1 << 16
+    bits = synth.rng(19).integers(0, 1 << 32, t, dtype=np.uint64).astype(np.uint32)
+    # halves (to even, both ways), their neighbours, the least and the largest values
+    edge = [h + d for h in (0x3F808000, 0x3F818000, 0x00008000, 0x00018000, 0x7F7F8000, 0x007F8000) for d in (-1, 0, 1)]
+    edge += [0, 1, 0x007FFFFF, 0x00800000, 0x7F7FFFFF, 0x7F800000]
+    edge = np.array(edge + [e | 0x80000000 for e in edge], np.uint32)
+    bits[:len(edge)] = edge
+    w = bits.view(np.float32)
+    x = torch.zeros((t, 128), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    codes = torch.zeros((1, 4, 128), dtype=torch.int8, device="cuda")
+    codes[:, :, 0] = 1
+    one = qg.QExperts(qg.QG_WFMT_INT8, 1, 4, 128, codes, torch.ones((1, 4), device="cuda"))
+    plan = qg.group_rows(torch.zeros((t, 1), dtype=torch.int32, device="cuda"), 1)
+    y = host(qg.qgemm_experts_combine(one, x, plan, dev(w.reshape(t, 1)), gather=True, y_dtype=torch.bfloat16))
+    nan = np.isnan(w)
+    with np.errstate(invalid="ignore"):
+        want = f32_to_bf16_rne(w + np.float32(0))  # a sum that starts at +0: no -0
+    assert np.array_equal(y[~nan], np.repeat(want[~nan, None], 4, axis=1))
+    assert np.isnan(bf16_to_f64(y[nan])).all() and nan.sum() > 100
 
 
 def test_long_k(qg):
