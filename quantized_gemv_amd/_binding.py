@@ -1055,8 +1055,10 @@ class LoraLaunch:
     (all kept alive by this object, with a workspace); launch() enqueues it on
     x's current stream. Launches that may overlap need objects of their own:
     they share ys and the workspace. The object may be dropped while launches
-    run, on any stream; while a graph that captured one may be replayed, it has
-    to be kept."""
+    run, on any stream: its own workspace waits for them. The tensors given to it
+    follow torch's rule (on a stream other than the one they were made on, they
+    are kept or recorded by the caller). While a graph that captured a launch may
+    be replayed, the object has to be kept."""
 
     def __init__(self, x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters],
                  ys: Sequence[torch.Tensor], ws: Optional[torch.Tensor] = None):
