@@ -73,6 +73,9 @@ typedef int32_t qg_status;
 /* element types */
 #define QG_F32  0
 #define QG_BF16 1
+/* 8-bit outputs of qg_rms_norm and qg_swiglu, with their scales */
+#define QG_INT8 2  /* int8, a multiplier 127 / max|v| per row (as QG_PER_ROW)       */
+#define QG_FP8  3  /* e4m3 (OCP: largest value 448, no infinities), a step per 128  */
 
 /* quantization granularity */
 #define QG_PER_TENSOR 0
@@ -91,6 +94,10 @@ typedef int32_t qg_status;
                               /* weight), [n][16 ceil(k/80)], per-tensor gamma      */
 #define QG_WFMT_INT8_T16   6  /* the codes of QG_WFMT_INT8 in 16-row tiles for the  */
                               /* batch products (qg_pack_tiles16), s_w[n]           */
+#define QG_WFMT_FP8        7  /* e4m3 codes [n][k], a step per block of 128 x 128:  */
+                              /* scale [ceil(n/128)][k/128] (qg_qgemm_fp8 only)     */
+#define QG_WFMT_FP8_T16    8  /* the codes of QG_WFMT_FP8 in 16-row tiles           */
+                              /* (qg_pack_tiles16), the same scale                  */
 
 /* activation modes of qg_qgemv */
 #define QG_ACT_INT8  0  /* x is quantized per tensor (absmax int8) inside the call */
@@ -114,6 +121,9 @@ typedef int32_t qg_status;
 #define QG_MAX_PLAN_ROWS (1 << 30)  /* rows of a row plan                             */
 #define QG_MAX_TOP_K    16      /* experts per token of qg_moe_route                  */
 #define QG_LORA_MAX_R   256     /* rank of a low-rank adapter                         */
+#define QG_FP8_BLOCK    128     /* values under one step of QG_FP8                    */
+#define QG_ROW_MAX_K    32768   /* row length where a row is kept on chip: the norm,
+                                   SwiGLU with int8 outputs                           */
 
 /* Human-readable text for a status code (static storage). */
 const char* qg_status_str(qg_status s);
@@ -870,6 +880,80 @@ typedef struct qg_lora {
 size_t qg_lora_workspace_bytes(const qg_lora* m, int32_t count, int64_t rows, int32_t groups, int64_t k);
 qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* groups, const void* x, int64_t x_rows,
                       int64_t k, int32_t yt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The 8-bit path between layers: what stands between two products (norm with
+ * the residual's addition, SwiGLU), with the next product's 8-bit input as
+ * output, 8-bit floating point (e4m3) in blocks of 128, and the product of
+ * such operands.  The pages describe none of it; the definitions here are this
+ * library's.  All arithmetic is fp32.  No gradients.
+ *
+ * e4m3 blocks.  A block is 128 consecutive values of a row (activations) or
+ * 128 x 128 values (weights; the last block of rows may have fewer):
+ *   a = max|v| of the block;  s = max(fl32(a / 448), 2^-126);  i = fl32(1 / s);
+ *   code = the e4m3 value nearest to fl32(v * i), ties to the even code;
+ * the code stands for code * s (s is a STEP, not a multiplier).  A block that
+ * holds an infinity or NaN has a NaN step and NaN codes (0x7F, 0xFF).  Steps of
+ * activations: [k/128][rows], those of one 128-slice of the columns together
+ * (as MXFP4's); of weights: [ceil(n/128)][k/128].
+ *
+ * qg_quantize_fp8       : x [rows][cols] of type xt (QG_F32 or QG_BF16) ->
+ *   q [rows][cols], s [cols/128][rows].  cols % 128 == 0, cols <= 2^30.
+ * qg_quantize_fp8_weight: w [n][k] of type wt -> codes [n][k], scale
+ *   [ceil(n/128)][k/128], as QG_WFMT_FP8 takes them.  k % 128 == 0, k <= 2^30.
+ *
+ * qg_rms_norm: h = x + residual (x where residual is NULL), in fp32;
+ *     v = h / sqrt(sum of h^2 over the row / k + eps) * weight;
+ *   residual_out = h rounded to xt (v goes on with h itself); may be residual
+ *   or x (in place).  y by out: QG_F32 or QG_BF16 (v rounded), QG_INT8 (codes
+ *   and s [rows] by the formulas of qg_quantize_absmax), QG_FP8 (codes and s
+ *   [k/128][rows]).  A row of int8 that holds an infinity or NaN has a NaN
+ *   multiplier.  x, residual, residual_out [rows][k] of type xt; weight [k] of
+ *   type wt; eps >= 2^-126.  8 <= k <= QG_ROW_MAX_K, k % 8 == 0 (k % 128 == 0
+ *   for QG_FP8).  s is ignored (may be NULL) for QG_F32 and QG_BF16.
+ *   residual and residual_out are both given or both NULL.
+ * qg_swiglu: x [rows][2 n] of type xt, gate's columns then up's (a product
+ *   with both matrices, one after the other);
+ *     v = g / (1 + exp(-g)) * u;
+ *   y [rows][n] and s by out as above.  n % 8 == 0 (n % 128 == 0 for QG_FP8);
+ *   n <= QG_ROW_MAX_K for QG_INT8, n <= 2^30 else.
+ *
+ * 1 <= rows < 2^31; rows * columns of x <= 2^40.  x, y, residual,
+ * residual_out, weight and w 16-B aligned, s 4-B.  Outputs must not overlap
+ * inputs or one another (QG_ERR_ARG), but for residual_out as above.
+ */
+qg_status qg_quantize_fp8(const void* x, int32_t xt, int64_t rows, int64_t cols, uint8_t* q, float* s,
+                          void* stream);
+qg_status qg_quantize_fp8_weight(const void* w, int32_t wt, int64_t n, int64_t k, uint8_t* codes, float* scale,
+                                 void* stream);
+qg_status qg_rms_norm(const void* x, int32_t xt, const void* residual, void* residual_out, const void* weight,
+                      int32_t wt, float eps, int64_t rows, int64_t k, int32_t out, void* y, float* s, void* stream);
+qg_status qg_swiglu(const void* x, int32_t xt, int64_t rows, int64_t n, int32_t out, void* y, float* s,
+                    void* stream);
+
+/*
+ * Product of e4m3 operands in blocks of 128, any number of tokens:
+ *   y[m][n] = sum over blocks b of s_x[b][m] s_w[n/128][b]
+ *             (sum of x[m][k] w[n][k] over the 128 k of b),
+ * y rounded once.  fp32 outputs: products exact, fp32 sums.  bf16 outputs: the
+ * same, or with many tokens the matrix cores' 8-bit instruction, which of every
+ * eight products (k = 8 j .. 8 j + 7) cuts off what lies below 2^-13 of the
+ * largest's binade: about 1.6e-5 of the result's size, against bf16's own
+ * rounding of up to 3.9e-3.  NaN codes and steps reach the outputs that they
+ * enter.
+ * w   : HOST descriptor, QG_WFMT_FP8 or QG_WFMT_FP8_T16: codes and scale are
+ *       device pointers, resid, scale2 and zero are ignored.
+ * x   : [m][k] e4m3 codes; s_x: [k/128][m] (qg_quantize_fp8, qg_rms_norm,
+ *       qg_swiglu).
+ * y   : [m][n] of type yt (QG_F32 or QG_BF16).
+ * k % 128 == 0, 128 <= k <= QG_BATCH_MAX_K; 1 <= m < 2^30; 1 <= n < 2^26;
+ * m * k and n * k <= 2^40, m * n <= 2^38.  codes, x and y 16-B aligned, the steps
+ * 4-B.  y must not overlap an input (QG_ERR_ARG).  Results are deterministic;
+ * which kernel runs depends on the sizes alone, and kernels differ in
+ * summation order.
+ */
+qg_status qg_qgemm_fp8(const qg_weight* w, const void* x, const float* s_x, int64_t m, void* y, int32_t yt,
+                       void* stream);
 
 /*
  * Measurement aid, not a step of the method: the streaming-read probe that

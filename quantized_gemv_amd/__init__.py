@@ -4,7 +4,8 @@ Python side of the C ABI in include/qgemv.h: symmetric absmax / absmean
 quantization to int8, ternary, sign + int8-residual, thresholded separated
 and group-wise 4-bit formats, bit packing, quantized GEMV for decode (batch 1
 and small batches), the W8A8 prefill GEMM with an activation outlier split,
-and an MXFP4 prefill on the FP4 matrix cores.  All arithmetic runs in the HIP kernels of
+an MXFP4 prefill on the FP4 matrix cores, and the 8-bit path between layers
+(norm, SwiGLU, e4m3 blocks of 128 and their product).  All arithmetic runs in the HIP kernels of
 libqgemv.so; this package only marshals arguments (see _binding.py).
 """
 from ._binding import (QgError, QWeight, CWeight, EXPORTED, LIB_PATH, lib, status_str,
@@ -20,6 +21,8 @@ from ._binding import (QgError, QWeight, CWeight, EXPORTED, LIB_PATH, lib, statu
                        RowGroups, Routing, group_rows, moe_route, QExperts, quantize_experts, tiled16_experts,
                        qgemm_experts, qgemm_experts_swiglu, qgemm_experts_combine, moe_ffn, LoraAdapters, LoraLaunch,
                        lora_add, CRowGroups, CExperts, CLora, QG_MAX_ROW_GROUPS, QG_MAX_PLAN_ROWS, QG_MAX_TOP_K,
-                       QG_LORA_MAX_R)
+                       QG_LORA_MAX_R,
+                       RmsNormLaunch, rms_norm, SwigluLaunch, swiglu, quantize_fp8, quantize_fp8_weight, QgemmFp8Launch,
+                       qgemm_fp8, fp8_ffn, QG_INT8, QG_FP8, QG_WFMT_FP8, QG_WFMT_FP8_T16, QG_FP8_BLOCK, QG_ROW_MAX_K)
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -21,9 +21,11 @@ LIB_PATH = os.path.join(_HERE, "libqgemv.so")
 QG_OK = 0
 QG_ERR_DEVICE_CHECK = 7  # QG_DEBUG=1 (or 2) only: a device-side check of the outlier path failed
 QG_F32, QG_BF16 = 0, 1
+QG_INT8, QG_FP8 = 2, 3
 QG_PER_TENSOR, QG_PER_ROW = 0, 1
 QG_WFMT_INT8, QG_WFMT_TERNARY2, QG_WFMT_SIGN1_RES8, QG_WFMT_Q4K, QG_WFMT_SIGN1_RES8Z, QG_WFMT_TERNARY3 = 0, 1, 2, 3, 4, 5
 QG_WFMT_INT8_T16 = 6
+QG_WFMT_FP8, QG_WFMT_FP8_T16 = 7, 8
 QG_ACT_INT8, QG_ACT_FLOAT = 0, 1
 QG_MAX_OUTLIERS = 256
 QG_QGEMV_MAX_K = 32768
@@ -40,6 +42,8 @@ QG_MAX_ROW_GROUPS = 1024
 QG_MAX_PLAN_ROWS = 1 << 30
 QG_MAX_TOP_K = 16
 QG_LORA_MAX_R = 256
+QG_FP8_BLOCK = 128
+QG_ROW_MAX_K = 32768
 QG_CHAIN_MAX_STAGES = 4096
 QG_CHAIN_MIN_K = 128
 QG_CHAIN_MAX_K = 16384
@@ -149,6 +153,12 @@ _SIGS = {
     "qg_lora_workspace_bytes": (_c_sz, [ctypes.POINTER(CLora), _c_i32, _c_i64, _c_i32, _c_i64]),
     "qg_lora_add": (_c_i32, [ctypes.POINTER(CLora), _c_i32, ctypes.POINTER(CRowGroups), _c_vp, _c_i64, _c_i64, _c_i32,
                              _c_vp, _c_sz, _c_vp]),
+    "qg_quantize_fp8": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "qg_quantize_fp8_weight": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "qg_rms_norm": (_c_i32, [_c_vp, _c_i32, _c_vp, _c_vp, _c_vp, _c_i32, ctypes.c_float, _c_i64, _c_i64, _c_i32, _c_vp,
+                             _c_vp, _c_vp]),
+    "qg_swiglu": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i32, _c_vp, _c_vp, _c_vp]),
+    "qg_qgemm_fp8": (_c_i32, [ctypes.POINTER(CWeight), _c_vp, _c_vp, _c_i64, _c_vp, _c_i32, _c_vp]),
     "qg_qgemm_w8a8": (_c_i32, [_c_vp, _c_vp, _c_vp, _c_i32, _c_i64, _c_i64, _c_i32, _c_vp, _c_vp, _c_vp, _c_i32,
                                _c_i64, _c_vp, _c_vp, _c_vp]),
 }
@@ -387,9 +397,12 @@ def pack_tiles16(codes: torch.Tensor, out: torch.Tensor = None):
 
 
 def tiled16(w: "QWeight") -> "QWeight":
-    """The QG_WFMT_INT8 matrix w with its codes in 16-row tiles."""
+    """The QG_WFMT_INT8 (or QG_WFMT_FP8) matrix w with its codes in 16-row tiles."""
+    if w.fmt == QG_WFMT_FP8:
+        t = pack_tiles16(w.codes.view(torch.int8).view(w.n, w.k))
+        return QWeight(QG_WFMT_FP8_T16, w.n, w.k, t.view(w.codes.dtype), w.scale)
     if w.fmt != QG_WFMT_INT8:
-        raise ValueError("tiled16 takes QG_WFMT_INT8 weights")
+        raise ValueError("tiled16 takes QG_WFMT_INT8 or QG_WFMT_FP8 weights")
     return QWeight(QG_WFMT_INT8_T16, w.n, w.k, pack_tiles16(w.codes.view(w.n, w.k)), w.scale)
 
 
@@ -1115,6 +1128,197 @@ def lora_add(x: torch.Tensor, groups: RowGroups, adapters: Sequence[LoraAdapters
     a y that requires one is refused while gradients are on. Returns ys."""
     LoraLaunch(x, groups, adapters, ys, ws).launch()
     return ys
+
+
+# ------------------------------------------------------------------ the 8-bit path between layers
+
+_OUT = {torch.float32: QG_F32, torch.bfloat16: QG_BF16, torch.int8: QG_INT8, torch.float8_e4m3fn: QG_FP8}
+
+
+def _rows_cols(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError("%s must be [rows][columns]" % name)
+    return t.shape
+
+
+def _out_dtype(y: Optional[torch.Tensor], dtype):
+    dt = dtype if y is None else y.dtype
+    if dt not in _OUT:
+        raise ValueError("outputs are float32, bfloat16, int8 or float8_e4m3fn")
+    return dt
+
+
+def _scale_out(s: Optional[torch.Tensor], dt, rows: int, cols: int, x: torch.Tensor):
+    """The scales of an 8-bit output (None for the others)."""
+    if dt not in (torch.int8, torch.float8_e4m3fn):
+        if s is not None:
+            raise ValueError("float outputs have no scales")
+        return None
+    return _shaped(s, "s", (rows,) if dt == torch.int8 else (cols // QG_FP8_BLOCK, rows), torch.float32, x)
+
+
+class _Launch:
+    """Pre-marshalled arguments of one call, with its outputs: launch() enqueues
+    it on x's current stream, again and again on the same memory. Launches that
+    may overlap need objects of their own. The tensors given to it, and its
+    outputs, follow torch's rule on other streams; the object, or what it
+    reads and writes, has to be kept while launches run and while a graph that
+    captured one may be replayed. No gradient passes."""
+
+    def _set(self, name: str, x: torch.Tensor, args, tensors, outs):
+        # x for its device; the memory itself, also if tensors' data is set anew
+        self._name, self._x = name, x.detach()
+        self._args, self._keep = args, _memory(*tensors)
+        self._outs = [t for t in outs if t is not None]
+
+    def launch(self):
+        for t in self._outs:
+            if t.requires_grad and torch.is_grad_enabled():
+                raise ValueError("outputs are written without a gradient: one requires a gradient")
+        _call(self._name, self._x, *self._args)
+        # a backward pass that has saved an output must see that it changed
+        torch._C._increment_version(self._outs)
+
+
+class RmsNormLaunch(_Launch):
+    """One qg_rms_norm call: x [rows][k] (fp32 or bf16), weight [k]; with a
+    residual (x's shape and type) its sum goes to residual_out (residual itself
+    by default). out_dtype, or y's: float32, bfloat16, int8 (s: a multiplier per
+    row) or float8_e4m3fn (s [k/128][rows]). Fields y, s, residual_out hold the
+    outputs."""
+
+    def __init__(self, x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, y: torch.Tensor = None,
+                 s: torch.Tensor = None):
+        _dev(x, "x", (torch.float32, torch.bfloat16))
+        rows, k = _rows_cols(x, "x")
+        _dev(weight, "weight", (torch.float32, torch.bfloat16))
+        if weight.shape != (k,):
+            raise ValueError("weight must be [%d]" % k)
+        _same_device(x, weight)
+        if residual is not None:
+            residual = _shaped(residual, "residual", x.shape, x.dtype, x)
+            residual_out = _shaped(residual if residual_out is None else residual_out, "residual_out", x.shape, x.dtype, x)
+        elif residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        dt = _out_dtype(y, out_dtype)
+        self.y, self.residual_out = _shaped(y, "y", (rows, k), dt, x), residual_out
+        self.s = _scale_out(s, dt, rows, k, x)
+        args = (_c_vp(_ptr(x)), _c_i32(_xt(x)), _c_vp(_ptr(residual)), _c_vp(_ptr(residual_out)), _c_vp(_ptr(weight)),
+                _c_i32(_xt(weight)), ctypes.c_float(eps), _c_i64(rows), _c_i64(k), _c_i32(_OUT[dt]), _c_vp(_ptr(self.y)),
+                _c_vp(_ptr(self.s)))
+        self._set("qg_rms_norm", x, args, (x, residual, weight, residual_out, self.y, self.s),
+                  (self.y, self.s, residual_out))
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             residual_out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, y: torch.Tensor = None,
+             s: torch.Tensor = None):
+    """Root-mean-square norm of the rows of x, or of x + residual
+    (qg_rms_norm, arguments as RmsNormLaunch); the sum replaces the residual
+    unless residual_out is given. Returns y, or (y, s) of 8-bit outputs."""
+    a = RmsNormLaunch(x, weight, eps, residual, residual_out, out_dtype, y, s)
+    a.launch()
+    return a.y if a.s is None else (a.y, a.s)
+
+
+class SwigluLaunch(_Launch):
+    """One qg_swiglu call: x [rows][2 n] (fp32 or bf16), gate's columns then
+    up's. out_dtype (or y's), y and s as RmsNormLaunch."""
+
+    def __init__(self, x: torch.Tensor, out_dtype=torch.bfloat16, y: torch.Tensor = None, s: torch.Tensor = None):
+        _dev(x, "x", (torch.float32, torch.bfloat16))
+        rows, n2 = _rows_cols(x, "x")
+        if n2 % 2:
+            raise ValueError("x must hold gate's and up's columns")
+        n, dt = n2 // 2, _out_dtype(y, out_dtype)
+        self.y = _shaped(y, "y", (rows, n), dt, x)
+        self.s = _scale_out(s, dt, rows, n, x)
+        args = (_c_vp(_ptr(x)), _c_i32(_xt(x)), _c_i64(rows), _c_i64(n), _c_i32(_OUT[dt]), _c_vp(_ptr(self.y)),
+                _c_vp(_ptr(self.s)))
+        self._set("qg_swiglu", x, args, (x, self.y, self.s), (self.y, self.s))
+
+
+def swiglu(x: torch.Tensor, out_dtype=torch.bfloat16, y: torch.Tensor = None, s: torch.Tensor = None):
+    """silu(gate) * up of x [rows][2 n] (qg_swiglu, arguments as SwigluLaunch).
+    Returns y [rows][n], or (y, s) of 8-bit outputs."""
+    a = SwigluLaunch(x, out_dtype, y, s)
+    a.launch()
+    return a.y if a.s is None else (a.y, a.s)
+
+
+def quantize_fp8(x: torch.Tensor, q: torch.Tensor = None, s: torch.Tensor = None):
+    """e4m3 codes of the rows of x [rows][cols] (fp32 or bf16), a step per 128
+    columns (qg_quantize_fp8). Returns (q float8_e4m3fn, s [cols/128][rows])."""
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    rows, cols = _rows_cols(x, "x")
+    q = _shaped(q, "q", (rows, cols), torch.float8_e4m3fn, x)
+    s = _shaped(s, "s", (cols // QG_FP8_BLOCK, rows), torch.float32, x)
+    _call("qg_quantize_fp8", x, x.data_ptr(), _xt(x), rows, cols, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def quantize_fp8_weight(w: torch.Tensor) -> QWeight:
+    """e4m3 codes of w [n][k] (fp32 or bf16), a step per block of 128 x 128
+    (qg_quantize_fp8_weight), as QG_WFMT_FP8. tiled16 lays them out in tiles."""
+    _dev(w, "w", (torch.float32, torch.bfloat16))
+    n, k = _rows_cols(w, "w")
+    codes = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=w.device)
+    scale = torch.empty((-(-n // QG_FP8_BLOCK), k // QG_FP8_BLOCK), dtype=torch.float32, device=w.device)
+    _call("qg_quantize_fp8_weight", w, w.data_ptr(), _xt(w), n, k, codes.data_ptr(), scale.data_ptr())
+    return QWeight(QG_WFMT_FP8, n, k, codes, scale)
+
+
+def _check_fp8_weight(w: QWeight):
+    if w.fmt not in (QG_WFMT_FP8, QG_WFMT_FP8_T16):
+        raise ValueError("weights must be QG_WFMT_FP8 or QG_WFMT_FP8_T16")
+    _dev(w.codes, "codes", (torch.float8_e4m3fn, torch.uint8, torch.int8))
+    _dev(w.scale, "scale", torch.float32)
+    _same_device(w.codes, w.scale)
+    n = -(-w.n // 16) * 16 if w.fmt == QG_WFMT_FP8_T16 else w.n
+    if w.codes.numel() != n * w.k or w.scale.numel() != -(-w.n // QG_FP8_BLOCK) * (w.k // QG_FP8_BLOCK):
+        raise ValueError("codes or scale do not hold a matrix of [%d][%d]" % (w.n, w.k))
+
+
+class QgemmFp8Launch(_Launch):
+    """One qg_qgemm_fp8 call: w (QG_WFMT_FP8 or QG_WFMT_FP8_T16), x
+    float8_e4m3fn [m][k] with its steps s_x [k/128][m]; the output is y [m][n]
+    (fp32 or bf16)."""
+
+    def __init__(self, w: QWeight, x: torch.Tensor, s_x: torch.Tensor, y_dtype=torch.bfloat16, y: torch.Tensor = None):
+        _check_fp8_weight(w)
+        _dev(x, "x", torch.float8_e4m3fn)
+        m, k = _rows_cols(x, "x")
+        if k != w.k:
+            raise ValueError("x must be [m][%d]" % w.k)
+        _dev(s_x, "s_x", torch.float32)
+        if s_x.shape != (k // QG_FP8_BLOCK, m):
+            raise ValueError("s_x must be [%d][%d]" % (k // QG_FP8_BLOCK, m))
+        _same_device(x, s_x, w.codes)
+        self.y = _shaped(y, "y", (m, w.n), _y_dtype(y, y_dtype), x)
+        self._w = w.c_struct()
+        args = (ctypes.pointer(self._w), _c_vp(_ptr(x)), _c_vp(_ptr(s_x)), _c_i64(m), _c_vp(_ptr(self.y)),
+                _c_i32(_xt(self.y)))
+        self._set("qg_qgemm_fp8", x, args, (x, s_x, w.codes, w.scale, self.y), (self.y,))
+
+
+def qgemm_fp8(w: QWeight, x: torch.Tensor, s_x: torch.Tensor, y_dtype=torch.bfloat16, y: torch.Tensor = None):
+    """Product of e4m3 operands in blocks of 128 (qg_qgemm_fp8, arguments as
+    QgemmFp8Launch), from one token to prefill. Returns y [m][n]."""
+    a = QgemmFp8Launch(w, x, s_x, y_dtype, y)
+    a.launch()
+    return a.y
+
+
+def fp8_ffn(x: torch.Tensor, residual: torch.Tensor, norm_weight: torch.Tensor, gate_up: QWeight, down: QWeight,
+            eps: float = 1e-6) -> torch.Tensor:
+    """A feed-forward layer on e4m3 weights: norm of x + residual (which becomes
+    the residual), gate and up in one product (their matrices one after the
+    other: [2 n][k]), SwiGLU, the way down. x bf16 [tokens][k]; returns bf16
+    [tokens][down.n], to be added to the residual by the next norm."""
+    q, s = rms_norm(x, norm_weight, eps, residual, out_dtype=torch.float8_e4m3fn)
+    h, s_h = swiglu(qgemm_fp8(gate_up, q, s), out_dtype=torch.float8_e4m3fn)
+    return qgemm_fp8(down, h, s_h)
 
 
 def chain_plan_image(stages, workgroups: int):

@@ -84,6 +84,37 @@ inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintp
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 inline bool fits(int64_t a, int64_t b) { return a <= kMaxElems / b; }  // a * b <= 2^40, b >= 1
 
+// Two ranges of bytes that share some (none does with an empty or null one).
+inline bool overlap(const void* p, uint64_t pb, const void* q, uint64_t qb) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && (a < b ? b - a < pb : a - b < qb) && pb && qb;
+}
+
+// Row operators with 8-bit outputs: bytes of y and s, and the checks they share
+// (x has `per` values per value of y).
+constexpr int64_t kMaxRowLen = (int64_t)1 << 30;
+uint64_t row_out_bytes(const qg::RowArgs& a) {
+    return (uint64_t)a.rows * (uint64_t)a.k * (a.out == QG_F32 ? 4 : a.out == QG_BF16 ? 2 : 1);
+}
+uint64_t row_scale_bytes(const qg::RowArgs& a) {
+    return a.out == QG_INT8 ? 4 * (uint64_t)a.rows
+                            : a.out == QG_FP8 ? 4 * (uint64_t)a.rows * (uint64_t)(a.k / QG_FP8_BLOCK) : 0;
+}
+qg_status check_rows(const qg::RowArgs& a, int64_t per, int64_t max_k) {
+    const bool scaled = a.out == QG_INT8 || a.out == QG_FP8;
+    if (!a.x || !a.y || (scaled && !a.s)) return QG_ERR_NULLPTR;
+    if (a.xt != QG_F32 && a.xt != QG_BF16) return QG_ERR_ARG;
+    if (!scaled && a.out != QG_F32 && a.out != QG_BF16) return QG_ERR_ARG;
+    if (a.rows < 1 || a.rows >= ((int64_t)1 << 31)) return QG_ERR_SHAPE;
+    if (a.k < 8 || a.k > max_k || a.k % (a.out == QG_FP8 ? QG_FP8_BLOCK : 8) != 0 || !fits(a.rows, per * a.k))
+        return QG_ERR_SHAPE;
+    if (!aligned16(a.x) || !aligned16(a.y) || (scaled && !aligned_to(a.s, 4))) return QG_ERR_ALIGN;
+    const uint64_t xb = (uint64_t)(a.rows * per) * (uint64_t)a.k * (a.xt == QG_F32 ? 4 : 2);
+    const uint64_t yb = row_out_bytes(a), sb = row_scale_bytes(a);
+    if (overlap(a.y, yb, a.x, xb) || overlap(a.s, sb, a.x, xb) || overlap(a.s, sb, a.y, yb)) return QG_ERR_ARG;
+    return QG_OK;
+}
+
 // A row plan as the products read it.
 qg_status check_groups(const qg_row_groups* g) {
     if (!g->offsets) return QG_ERR_NULLPTR;
@@ -875,6 +906,109 @@ qg_status qg_lora_add(const qg_lora* m, int32_t count, const qg_row_groups* grou
     a.rows = groups->rows;
     a.ws = ws;
     return from_hip(qg::launch_lora(a, as_stream(stream)));
+}
+
+qg_status qg_quantize_fp8(const void* x, int32_t xt, int64_t rows, int64_t cols, uint8_t* q, float* s,
+                          void* stream) {
+    qg::RowArgs a = {};
+    a.x = x;
+    a.xt = xt;
+    a.rows = rows;
+    a.k = cols;
+    a.out = QG_FP8;
+    a.y = q;
+    a.s = s;
+    const qg_status st = check_rows(a, 1, kMaxRowLen);
+    if (st != QG_OK) return st;
+    return from_hip(qg::launch_quantize_fp8(a, as_stream(stream)));
+}
+
+qg_status qg_quantize_fp8_weight(const void* w, int32_t wt, int64_t n, int64_t k, uint8_t* codes, float* scale,
+                                 void* stream) {
+    if (!w || !codes || !scale) return QG_ERR_NULLPTR;
+    if (wt != QG_F32 && wt != QG_BF16) return QG_ERR_ARG;
+    if (n < 1 || n >= ((int64_t)1 << 31) || k < QG_FP8_BLOCK || k % QG_FP8_BLOCK != 0 || k > kMaxRowLen || !fits(n, k))
+        return QG_ERR_SHAPE;
+    if (!aligned16(w) || !aligned16(codes) || !aligned_to(scale, 4)) return QG_ERR_ALIGN;
+    const uint64_t nk = (uint64_t)n * (uint64_t)k;
+    const uint64_t ns = 4 * (uint64_t)((n + QG_FP8_BLOCK - 1) / QG_FP8_BLOCK) * (uint64_t)(k / QG_FP8_BLOCK);
+    const uint64_t wb = nk * (wt == QG_F32 ? 4 : 2);
+    if (overlap(codes, nk, w, wb) || overlap(scale, ns, w, wb) || overlap(scale, ns, codes, nk)) return QG_ERR_ARG;
+    return from_hip(qg::launch_quantize_fp8_weight(w, wt, n, k, codes, scale, as_stream(stream)));
+}
+
+qg_status qg_rms_norm(const void* x, int32_t xt, const void* residual, void* residual_out, const void* weight,
+                      int32_t wt, float eps, int64_t rows, int64_t k, int32_t out, void* y, float* s,
+                      void* stream) {
+    if (!weight || !residual != !residual_out) return QG_ERR_NULLPTR;
+    if ((wt != QG_F32 && wt != QG_BF16) || !(eps >= 1.17549435e-38f) || eps > 3.40282347e38f) return QG_ERR_ARG;
+    qg::RowArgs a = {};
+    a.x = x;
+    a.xt = xt;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.weight = weight;
+    a.wt = wt;
+    a.eps = eps;
+    a.rows = rows;
+    a.k = k;
+    a.out = out;
+    a.y = y;
+    a.s = s;
+    const qg_status st = check_rows(a, 1, QG_ROW_MAX_K);
+    if (st != QG_OK) return st;
+    if (!aligned16(weight) || !aligned16(residual) || !aligned16(residual_out)) return QG_ERR_ALIGN;
+    const uint64_t wb = (uint64_t)k * (wt == QG_F32 ? 4 : 2), xb = (uint64_t)rows * (uint64_t)k * (xt == QG_F32 ? 4 : 2);
+    const uint64_t yb = row_out_bytes(a), sb = row_scale_bytes(a);
+    if (overlap(y, yb, weight, wb) || overlap(s, sb, weight, wb)) return QG_ERR_ARG;
+    if (residual) {
+        if (overlap(y, yb, residual, xb) || overlap(s, sb, residual, xb) || overlap(y, yb, residual_out, xb) ||
+            overlap(s, sb, residual_out, xb) || overlap(residual_out, xb, weight, wb))
+            return QG_ERR_ARG;
+        if ((residual_out != residual && overlap(residual_out, xb, residual, xb)) ||
+            (residual_out != x && overlap(residual_out, xb, x, xb)))
+            return QG_ERR_ARG;
+    }
+    return from_hip(qg::launch_rms_norm(a, as_stream(stream)));
+}
+
+qg_status qg_swiglu(const void* x, int32_t xt, int64_t rows, int64_t n, int32_t out, void* y, float* s,
+                    void* stream) {
+    qg::RowArgs a = {};
+    a.x = x;
+    a.xt = xt;
+    a.rows = rows;
+    a.k = n;
+    a.out = out;
+    a.y = y;
+    a.s = s;
+    const qg_status st = check_rows(a, 2, out == QG_INT8 ? QG_ROW_MAX_K : kMaxRowLen);
+    if (st != QG_OK) return st;
+    return from_hip(qg::launch_swiglu(a, as_stream(stream)));
+}
+
+qg_status qg_qgemm_fp8(const qg_weight* w, const void* x, const float* s_x, int64_t m, void* y, int32_t yt,
+                       void* stream) {
+    if (!w || !x || !s_x || !y || !w->codes || !w->scale) return QG_ERR_NULLPTR;
+    if (w->fmt != QG_WFMT_FP8 && w->fmt != QG_WFMT_FP8_T16) return QG_ERR_ARG;
+    if (yt != QG_F32 && yt != QG_BF16) return QG_ERR_ARG;
+    const int64_t n = w->n, k = w->k;
+    if (k < QG_FP8_BLOCK || k % QG_FP8_BLOCK != 0 || k > QG_BATCH_MAX_K) return QG_ERR_SHAPE;
+    if (m < 1 || m >= ((int64_t)1 << 30) || n < 1 || n >= ((int64_t)1 << 26)) return QG_ERR_SHAPE;
+    if (!fits(m, k) || !fits(n, k) || !fits(m, 4 * n)) return QG_ERR_SHAPE;
+    if (!aligned16(w->codes) || !aligned16(x) || !aligned16(y)) return QG_ERR_ALIGN;
+    if (!aligned_to(w->scale, 4) || !aligned_to(s_x, 4)) return QG_ERR_ALIGN;
+    const bool t16 = w->fmt == QG_WFMT_FP8_T16;
+    const uint64_t kb = (uint64_t)(k / QG_FP8_BLOCK);
+    const uint64_t yb = (uint64_t)m * (uint64_t)n * (yt == QG_F32 ? 4 : 2);
+    const uint64_t wb = (uint64_t)(t16 ? (n + 15) / 16 * 16 : n) * (uint64_t)k;
+    if (overlap(y, yb, w->codes, wb) || overlap(y, yb, x, (uint64_t)m * (uint64_t)k) ||
+        overlap(y, yb, s_x, 4 * kb * (uint64_t)m) ||
+        overlap(y, yb, w->scale, 4 * kb * (uint64_t)((n + QG_FP8_BLOCK - 1) / QG_FP8_BLOCK)))
+        return QG_ERR_ARG;
+    const qg::Fp8GemmArgs a = {static_cast<const uint8_t*>(w->codes), w->scale, t16, static_cast<const uint8_t*>(x),
+                               s_x, m, n, k, y, yt};
+    return from_hip(qg::launch_qgemm_fp8(a, as_stream(stream)));
 }
 
 size_t qg_probe_stream_read_bytes(int64_t bytes, int32_t workgroups) {

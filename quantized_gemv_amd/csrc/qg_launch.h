@@ -217,6 +217,40 @@ size_t lora_workspace(int64_t rows, int64_t groups, int64_t k, int count, int rm
                       int64_t padded_rank);
 hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
 
+// Rows through a norm, SwiGLU or nothing, out as fp32 (0), bf16 (1), int8 with a
+// multiplier per row (2) or e4m3 in blocks of 128 (3).
+struct RowArgs {
+    const void* x;
+    int xt;
+    const void* residual;  // norm: added to x, or null
+    void* residual_out;
+    const void* weight;
+    int wt;
+    float eps;
+    int64_t rows, k;       // k: values of an output row
+    int out;
+    void* y;
+    float* s;              // int8: [rows]; e4m3: [k / 128][rows]
+};
+hipError_t launch_rms_norm(const RowArgs& a, hipStream_t st);
+hipError_t launch_swiglu(const RowArgs& a, hipStream_t st);
+hipError_t launch_quantize_fp8(const RowArgs& a, hipStream_t st);
+hipError_t launch_quantize_fp8_weight(const void* w, int wt, int64_t n, int64_t k, uint8_t* codes, float* scale,
+                                      hipStream_t st);
+
+// Product of e4m3 operands in blocks of 128: y[m][n], fp32 (0) or bf16 (1).
+struct Fp8GemmArgs {
+    const uint8_t* codes;  // [n][k], or 16-row tiles
+    const float* s_w;      // [ceil(n / 128)][k / 128]
+    bool t16;
+    const uint8_t* x;      // [m][k]
+    const float* s_x;      // [k / 128][m]
+    int64_t m, n, k;
+    void* y;
+    int yt;
+};
+hipError_t launch_qgemm_fp8(const Fp8GemmArgs& a, hipStream_t st);
+
 int device_cu_count();
 
 // Streaming-read probe: workgroups of kQProbeThreads each read one block of
