@@ -948,12 +948,17 @@ qg_status qg_swiglu(const void* x, int32_t xt, int64_t rows, int64_t n, int32_t 
  * y   : [m][n] of type yt (QG_F32 or QG_BF16).
  * k % 128 == 0, 128 <= k <= QG_BATCH_MAX_K; 1 <= m < 2^30; 1 <= n < 2^26;
  * m * k and n * k <= 2^40, m * n <= 2^38.  codes, x and y 16-B aligned, the steps
- * 4-B.  y must not overlap an input (QG_ERR_ARG).  Results are deterministic;
- * which kernel runs depends on the sizes alone, and kernels differ in
- * summation order.
+ * 4-B.  y and ws must not overlap an input or each other (QG_ERR_ARG).
+ * ws  : qg_qgemm_fp8_workspace_bytes(m, n, k, yt) bytes, 16-B aligned (may be
+ *       NULL when that is 0: the fp32 sums of parts of k, at most 8 m n values,
+ *       where the tiles are few); its contents on entry do not matter.  Calls
+ *       that overlap on one workspace race.
+ * Results are deterministic; which kernel runs depends on the sizes and yt
+ * alone, and kernels differ in summation order.
  */
+size_t qg_qgemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t yt);  /* 0 if out of range, too */
 qg_status qg_qgemm_fp8(const qg_weight* w, const void* x, const float* s_x, int64_t m, void* y, int32_t yt,
-                       void* stream);
+                       void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Measurement aid, not a step of the method: the streaming-read probe that

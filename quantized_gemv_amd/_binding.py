@@ -158,7 +158,8 @@ _SIGS = {
     "qg_rms_norm": (_c_i32, [_c_vp, _c_i32, _c_vp, _c_vp, _c_vp, _c_i32, ctypes.c_float, _c_i64, _c_i64, _c_i32, _c_vp,
                              _c_vp, _c_vp]),
     "qg_swiglu": (_c_i32, [_c_vp, _c_i32, _c_i64, _c_i64, _c_i32, _c_vp, _c_vp, _c_vp]),
-    "qg_qgemm_fp8": (_c_i32, [ctypes.POINTER(CWeight), _c_vp, _c_vp, _c_i64, _c_vp, _c_i32, _c_vp]),
+    "qg_qgemm_fp8_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "qg_qgemm_fp8": (_c_i32, [ctypes.POINTER(CWeight), _c_vp, _c_vp, _c_i64, _c_vp, _c_i32, _c_vp, _c_sz, _c_vp]),
     "qg_qgemm_w8a8": (_c_i32, [_c_vp, _c_vp, _c_vp, _c_i32, _c_i64, _c_i64, _c_i32, _c_vp, _c_vp, _c_vp, _c_i32,
                                _c_i64, _c_vp, _c_vp, _c_vp]),
 }
@@ -1160,14 +1161,18 @@ def _scale_out(s: Optional[torch.Tensor], dt, rows: int, cols: int, x: torch.Ten
 class _Launch:
     """Pre-marshalled arguments of one call, with its outputs: launch() enqueues
     it on x's current stream, again and again on the same memory. Launches that
-    may overlap need objects of their own. The tensors given to it, and its
-    outputs, follow torch's rule on other streams; the object, or what it
-    reads and writes, has to be kept while launches run and while a graph that
-    captured one may be replayed. No gradient passes."""
+    may overlap need objects of their own: they share the outputs and the
+    workspace. The object may be dropped while launches run, on any stream: a
+    workspace of its own waits for them. The tensors given to it, and its
+    outputs, follow torch's rule (on a stream other than the one they were made
+    on, they are kept or recorded by the caller). While a graph that captured a
+    launch may be replayed, the object has to be kept. No gradient passes."""
 
-    def _set(self, name: str, x: torch.Tensor, args, tensors, outs):
+    def _set(self, name: str, x: torch.Tensor, args, tensors, outs, own_ws: Optional[torch.Tensor] = None):
         # x for its device; the memory itself, also if tensors' data is set anew
         self._name, self._x = name, x.detach()
+        # a workspace of this object's own, and the stream that it comes from
+        self._ws, self._made_on = own_ws, None if own_ws is None else _raw_stream(x.get_device())
         self._args, self._keep = args, _memory(*tensors)
         self._outs = [t for t in outs if t is not None]
 
@@ -1175,6 +1180,10 @@ class _Launch:
         for t in self._outs:
             if t.requires_grad and torch.is_grad_enabled():
                 raise ValueError("outputs are written without a gradient: one requires a gradient")
+        if self._ws is not None and _raw_stream(self._x.get_device()) != self._made_on:
+            # no one else knows of this use: once dropped, it would go to the next
+            # tensor of its own stream while the kernels still run
+            self._ws.record_stream(torch.cuda.current_stream(self._x.device))
         _call(self._name, self._x, *self._args)
         # a backward pass that has saved an output must see that it changed
         torch._C._increment_version(self._outs)
@@ -1283,9 +1292,10 @@ def _check_fp8_weight(w: QWeight):
 class QgemmFp8Launch(_Launch):
     """One qg_qgemm_fp8 call: w (QG_WFMT_FP8 or QG_WFMT_FP8_T16), x
     float8_e4m3fn [m][k] with its steps s_x [k/128][m]; the output is y [m][n]
-    (fp32 or bf16)."""
+    (fp32 or bf16). ws: uint8, qg_qgemm_fp8_workspace_bytes, or the object's own."""
 
-    def __init__(self, w: QWeight, x: torch.Tensor, s_x: torch.Tensor, y_dtype=torch.bfloat16, y: torch.Tensor = None):
+    def __init__(self, w: QWeight, x: torch.Tensor, s_x: torch.Tensor, y_dtype=torch.bfloat16, y: torch.Tensor = None,
+                 ws: Optional[torch.Tensor] = None):
         _check_fp8_weight(w)
         _dev(x, "x", torch.float8_e4m3fn)
         m, k = _rows_cols(x, "x")
@@ -1297,15 +1307,19 @@ class QgemmFp8Launch(_Launch):
         _same_device(x, s_x, w.codes)
         self.y = _shaped(y, "y", (m, w.n), _y_dtype(y, y_dtype), x)
         self._w = w.c_struct()
+        need = int(lib().qg_qgemm_fp8_workspace_bytes(m, w.n, k, _xt(self.y)))
+        ws_t, nws = _workspace(ws, need, x)
         args = (ctypes.pointer(self._w), _c_vp(_ptr(x)), _c_vp(_ptr(s_x)), _c_i64(m), _c_vp(_ptr(self.y)),
-                _c_i32(_xt(self.y)))
-        self._set("qg_qgemm_fp8", x, args, (x, s_x, w.codes, w.scale, self.y), (self.y,))
+                _c_i32(_xt(self.y)), _c_vp(_ptr(ws_t)), _c_sz(nws))
+        self._set("qg_qgemm_fp8", x, args, (x, s_x, w.codes, w.scale, self.y, ws_t), (self.y,),
+                  ws_t if ws is None else None)
 
 
-def qgemm_fp8(w: QWeight, x: torch.Tensor, s_x: torch.Tensor, y_dtype=torch.bfloat16, y: torch.Tensor = None):
+def qgemm_fp8(w: QWeight, x: torch.Tensor, s_x: torch.Tensor, y_dtype=torch.bfloat16, y: torch.Tensor = None,
+              ws: Optional[torch.Tensor] = None):
     """Product of e4m3 operands in blocks of 128 (qg_qgemm_fp8, arguments as
     QgemmFp8Launch), from one token to prefill. Returns y [m][n]."""
-    a = QgemmFp8Launch(w, x, s_x, y_dtype, y)
+    a = QgemmFp8Launch(w, x, s_x, y_dtype, y, ws)
     a.launch()
     return a.y
 

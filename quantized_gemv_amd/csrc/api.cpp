@@ -115,6 +115,12 @@ qg_status check_rows(const qg::RowArgs& a, int64_t per, int64_t max_k) {
     return QG_OK;
 }
 
+qg_status check_fp8_sizes(int64_t m, int64_t n, int64_t k) {
+    if (k < QG_FP8_BLOCK || k % QG_FP8_BLOCK != 0 || k > QG_BATCH_MAX_K) return QG_ERR_SHAPE;
+    if (m < 1 || m >= ((int64_t)1 << 30) || n < 1 || n >= ((int64_t)1 << 26)) return QG_ERR_SHAPE;
+    return fits(m, k) && fits(n, k) && fits(m, 4 * n) ? QG_OK : QG_ERR_SHAPE;
+}
+
 // A row plan as the products read it.
 qg_status check_groups(const qg_row_groups* g) {
     if (!g->offsets) return QG_ERR_NULLPTR;
@@ -987,27 +993,39 @@ qg_status qg_swiglu(const void* x, int32_t xt, int64_t rows, int64_t n, int32_t 
     return from_hip(qg::launch_swiglu(a, as_stream(stream)));
 }
 
+size_t qg_qgemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t yt) {
+    if (check_fp8_sizes(m, n, k) != QG_OK || (yt != QG_F32 && yt != QG_BF16)) return 0;
+    return qg::fp8_workspace(m, n, k, yt);
+}
+
 qg_status qg_qgemm_fp8(const qg_weight* w, const void* x, const float* s_x, int64_t m, void* y, int32_t yt,
-                       void* stream) {
+                       void* ws, size_t ws_bytes, void* stream) {
     if (!w || !x || !s_x || !y || !w->codes || !w->scale) return QG_ERR_NULLPTR;
     if (w->fmt != QG_WFMT_FP8 && w->fmt != QG_WFMT_FP8_T16) return QG_ERR_ARG;
     if (yt != QG_F32 && yt != QG_BF16) return QG_ERR_ARG;
     const int64_t n = w->n, k = w->k;
-    if (k < QG_FP8_BLOCK || k % QG_FP8_BLOCK != 0 || k > QG_BATCH_MAX_K) return QG_ERR_SHAPE;
-    if (m < 1 || m >= ((int64_t)1 << 30) || n < 1 || n >= ((int64_t)1 << 26)) return QG_ERR_SHAPE;
-    if (!fits(m, k) || !fits(n, k) || !fits(m, 4 * n)) return QG_ERR_SHAPE;
+    const qg_status st = check_fp8_sizes(m, n, k);
+    if (st != QG_OK) return st;
     if (!aligned16(w->codes) || !aligned16(x) || !aligned16(y)) return QG_ERR_ALIGN;
     if (!aligned_to(w->scale, 4) || !aligned_to(s_x, 4)) return QG_ERR_ALIGN;
     const bool t16 = w->fmt == QG_WFMT_FP8_T16;
     const uint64_t kb = (uint64_t)(k / QG_FP8_BLOCK);
     const uint64_t yb = (uint64_t)m * (uint64_t)n * (yt == QG_F32 ? 4 : 2);
     const uint64_t wb = (uint64_t)(t16 ? (n + 15) / 16 * 16 : n) * (uint64_t)k;
-    if (overlap(y, yb, w->codes, wb) || overlap(y, yb, x, (uint64_t)m * (uint64_t)k) ||
-        overlap(y, yb, s_x, 4 * kb * (uint64_t)m) ||
-        overlap(y, yb, w->scale, 4 * kb * (uint64_t)((n + QG_FP8_BLOCK - 1) / QG_FP8_BLOCK)))
+    const uint64_t xb = (uint64_t)m * (uint64_t)k, sb = 4 * kb * (uint64_t)m;
+    const uint64_t swb = 4 * kb * (uint64_t)((n + QG_FP8_BLOCK - 1) / QG_FP8_BLOCK);
+    if (overlap(y, yb, w->codes, wb) || overlap(y, yb, x, xb) || overlap(y, yb, s_x, sb) || overlap(y, yb, w->scale, swb))
         return QG_ERR_ARG;
+    const size_t need = qg::fp8_workspace(m, n, k, yt);
+    if (need) {
+        if (!ws || ws_bytes < need) return QG_ERR_WORKSPACE;
+        if (!aligned16(ws)) return QG_ERR_ALIGN;
+        if (overlap(ws, need, y, yb) || overlap(ws, need, w->codes, wb) || overlap(ws, need, x, xb) ||
+            overlap(ws, need, s_x, sb) || overlap(ws, need, w->scale, swb))
+            return QG_ERR_ARG;
+    }
     const qg::Fp8GemmArgs a = {static_cast<const uint8_t*>(w->codes), w->scale, t16, static_cast<const uint8_t*>(x),
-                               s_x, m, n, k, y, yt};
+                               s_x, m, n, k, y, yt, ws};
     return from_hip(qg::launch_qgemm_fp8(a, as_stream(stream)));
 }
 

@@ -33,6 +33,9 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int64_t kCUs = 256;  // MI355X
+constexpr int kMaxParts = 8;  // of k
+
 struct Fp8Params {
     const uint8_t* codes;
     const float* s_w;
@@ -42,7 +45,11 @@ struct Fp8Params {
     int K, KB;  // KB = K / 128
     void* y;
     int yt;
-    int tiles_m, tiles_n;
+    // tile kernels: the matrix rows from n1 on go in the second kind of tile; parts
+    // of k, their sums [parts][M][ld] in fp32 where there is more than one
+    int64_t n1;
+    int tiles_m, tiles_n, tiles_m2, tiles_n2, parts;
+    float* sums;
 };
 
 // 32 codes of a row as the matrix instructions take them.
@@ -89,31 +96,40 @@ __device__ __forceinline__ f32x4 block_product(const Operand<WIDE>& a, const Ope
     return d;
 }
 
-// Four outputs of one token, columns n .. n + 3 (those below N).
-__device__ __forceinline__ void store4(const Fp8Params& p, int64_t m, int64_t n, f32x4 v) {
-    const int64_t at = m * p.N + n;
-    const bool whole = (p.N & 3) == 0;  // then n + 3 < N, and the address is a multiple of the store
-    if (p.yt == 0) {
-        float* y = static_cast<float*>(p.y) + at;
-        if (whole) {
+// Where outputs go: rows of ld values, of which the first n exist; whole: every
+// four columns from a multiple of 4 can be stored at once.
+struct Out {
+    void* y;
+    int yt;  // 0: fp32, 1: bf16
+    int64_t ld, n;
+    bool whole;
+};
+
+// Four outputs of one token, columns n .. n + 3 (n < o.n).
+__device__ __forceinline__ void store4(const Out& o, int64_t m, int64_t n, f32x4 v) {
+    const int64_t at = m * o.ld + n;
+    if (o.yt == 0) {
+        float* y = static_cast<float*>(o.y) + at;
+        if (o.whole) {
             *reinterpret_cast<f32x4*>(y) = v;
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n + i < p.N) y[i] = v[i];
+                if (n + i < o.n) y[i] = v[i];
         }
     } else {
-        uint16_t* y = static_cast<uint16_t*>(p.y) + at;
-        if (whole) {
+        uint16_t* y = static_cast<uint16_t*>(o.y) + at;
+        if (o.whole) {
             *reinterpret_cast<uint2*>(y) = make_uint2(any_f32_to_bf16(v[0]) | (any_f32_to_bf16(v[1]) << 16),
                                                       any_f32_to_bf16(v[2]) | (any_f32_to_bf16(v[3]) << 16));
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n + i < p.N) y[i] = (uint16_t)any_f32_to_bf16(v[i]);
+                if (n + i < o.n) y[i] = (uint16_t)any_f32_to_bf16(v[i]);
         }
     }
 }
+__device__ __forceinline__ Out output_of(const Fp8Params& p) { return {p.y, p.yt, p.N, p.N, (p.N & 3) == 0}; }
 
 // ------------------------------------------------------------------ few tokens
 // The time goes into reading the matrix once.  A workgroup multiplies 16 RT
@@ -141,7 +157,11 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
 #pragma unroll
     for (int t = 0; t < RT; ++t)
         wo[t] = TILED ? (uint32_t)min(t, rw / 16 - 1) * 16u * (uint32_t)p.K + 16u * lane
-                      : (uint32_t)min(16 * t + r, rw - 1) * (uint32_t)p.K + 16u * g;
+                      : (uint32_t)min(16 * t + (r & 7), rw - 1) * (uint32_t)p.K + 16u * g + 64u * (r >> 3);
+    uint32_t wo8[RT];  // row-major: rows 8 .. 15 of each 16
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        wo8[t] = (uint32_t)min(16 * t + 8 + (r & 7), rw - 1) * (uint32_t)p.K + 16u * g + 64u * (r >> 3);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int m = min(16 * t + r, rx - 1);
@@ -159,7 +179,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
         for (int t = 0; t < RT; ++t) {
             const uint32_t o = in ? wo[t] + ws : w_bytes;
             wb[u][t][0] = load16(wr, o);
-            wb[u][t][1] = load16(wr, in ? o + (TILED ? 1024u : 64u) : w_bytes);
+            wb[u][t][1] = load16(wr, !in ? w_bytes : TILED ? o + 1024u : wo8[t] + ws);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -180,6 +200,20 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
     for (int kb = wave; kb < p.KB; kb += NW * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            // Row-major rows are loaded in whole lines, eight rows at a time: lane
+            // (r, g) holds bytes 16 g + 64 (r / 8) of rows r % 8 and 8 + r % 8.
+            // Lanes r and r ^ 8 exchange what belongs to the other's row.
+            if constexpr (!TILED) {
+#pragma unroll
+                for (int b = 0; b < RT; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t lo = wb[u][b][0][i], hi = wb[u][b][1][i];
+                        const uint32_t got = (uint32_t)dpp_mov<0x128>((int)(r < 8 ? hi : lo));  // row_ror:8
+                        wb[u][b][0][i] = r < 8 ? lo : got;
+                        wb[u][b][1][i] = r < 8 ? got : hi;
+                    }
+            }
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
                 const Operand<WIDE> bx = operand<WIDE>(xb[u][a][0], xb[u][a][1]);
@@ -199,6 +233,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
 #pragma unroll
         for (int b = 0; b < RT; ++b) red[wave][a * RT + b][lane] = acc[a][b];
     __syncthreads();
+    const Out o = output_of(p);
     for (int q = threadIdx.x; q < MT * RT * 64; q += 64 * NW) {
         const int t = q >> 6, l = q & 63;
         f32x4 v = red[0][t][l];
@@ -206,97 +241,113 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
         for (int w = 1; w < NW; ++w) v += red[w][t][l];
         const int64_t m = m0 + 16 * (t / RT) + (l & 15);
         const int64_t n = 16 * (tile0 + t % RT) + 4 * (l >> 4);
-        if (m < p.M && n < p.N) store4(p, m, n, v);
+        if (m < p.M && n < p.N) store4(o, m, n, v);
     }
 }
 
 // ------------------------------------------------------------------ many tokens
-// A workgroup computes BM tokens x BN matrix rows; both operands go through a
-// ring of STAGES LDS buffers of one block of k each, filled by direct
-// global -> LDS loads.  Rows of 128 bytes are stored with their 16-byte chunks
-// permuted by the row (swz), 16-row tiles as they are: both are read without
-// bank conflicts.
-
-template <int LPS, int MAXL>
-__device__ __forceinline__ void wait_later(int later) {
-    if constexpr (MAXL > 0) {
-        if (later >= MAXL) wait_vmcnt<MAXL * LPS>();
-        else wait_later<LPS, MAXL - 1>(later);
-    } else {
-        wait_vmcnt<0>();
-    }
-}
-
-template <int BM_, int BN_, int WAVES_M, int WAVES_N, int STAGES>
+// A workgroup of WAVES_M x WAVES_N waves computes BM tokens x BN matrix rows
+// over KB / parts blocks of k.  Both operands go through STAGES LDS buffers of
+// a block each, filled by direct global -> LDS loads; rows of 128 bytes are
+// stored with their 16-byte chunks permuted by the row (swz), 16-row tiles as
+// they are: both are read without bank conflicts.
+//
+// What bounds it is the loads into LDS (from the L2s about 65 bytes per ns and
+// CU with all of them at work), so they never stop: a buffer is refilled in two
+// parts while its block is still multiplied.  The matrix rows' fragments and
+// those of the first half of a wave's tokens are in registers first (a
+// group of 16 tokens is read LA groups ahead); once every wave has them, that
+// part is requested again (S1), the second half when that is read (S2), each
+// 1.5 blocks before it is wanted.  The loads are spread between the matrix
+// instructions (at once, a wave would stand still until the address unit has
+// taken all of them: 2.45 -> 2.57 PFLOP/s at 4096 x 4096 x 16384), and the
+// products of kLag instructions ago take their steps beside them.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_>
 struct Fp8Tile {
-    static constexpr int BM = BM_, BN = BN_, kNW = WAVES_M * WAVES_N;
+    static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
+    static constexpr int kNW = WAVES_M * WAVES_N;
     static constexpr int MT = BM / WAVES_M / 16, NT = BN / WAVES_N / 16;
     static constexpr int kCodes = (BM + BN) * kFp8Block;
-    static constexpr int kScaleLoads = BM / 64 + 1;  // 64 steps of x each, then those of w
-    static constexpr int kStage = kCodes + 256 * kScaleLoads;
-    static constexpr int kData = kCodes / 1024 / kNW;
-    static constexpr int kLPS = kData + 1;
-    static_assert(kCodes / 1024 % kNW == 0 && kScaleLoads <= kNW && BM % 64 == 0 && kFp8Block % (BN / WAVES_N) == 0,
+    static constexpr int kHalf = BM / 16 / kNW;      // 1 KB loads per wave: half of x's rows,
+    static constexpr int kW = BN / 8 / kNW;          // all of the matrix's,
+    static constexpr int kScaleLoads = BM / 64 + 1;  // and of all waves 64 steps of x each, then those of w
+    static constexpr int kSL = (kScaleLoads + kNW - 1) / kNW;
+    static constexpr int kScales = 256 * kScaleLoads;
+    static constexpr int kFirst = kW + kHalf + kSL, kSecond = kHalf;  // loads of a block's two parts
+    static_assert(BM % (16 * kNW) == 0 && BN % (8 * kNW) == 0 && BM % 64 == 0 && kFp8Block % (BN / WAVES_N) == 0,
                   "whole loads per wave, one step of w per wave");
-    static constexpr int kLds = STAGES * kStage;
+    static constexpr int kLds = STAGES * kCodes + (STAGES + 1) * kScales;
 };
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, bool TILED, bool WIDE>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void fp8_tile_kernel(Fp8Params p) {
-    typedef Fp8Tile<BM, BN, WAVES_M, WAVES_N, STAGES> C;
+template <class C, bool TILED, bool WIDE>
+__device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int64_t m0, int64_t n0, int kb0, int kb1,
+                                         const Out& out) {
+    constexpr int BM = C::BM, BN = C::BN, WAVES_M = C::WAVES_M, WAVES_N = C::WAVES_N, STAGES = C::STAGES;
     constexpr int MT = C::MT, NT = C::NT, NW = C::kNW;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
-
-    // tiles in supertiles of 4 token tiles, a contiguous run of them per XCD
-    const int t = (int)xcd_run(blockIdx.x, gridDim.x);
-    const int per = 4 * p.tiles_n;
-    const int st = t / per, u = t - st * per;
-    const int h = min(4, p.tiles_m - 4 * st);
-    const int64_t m0 = (int64_t)(4 * st + u % h) * BM, n0 = (int64_t)(u / h) * BN;
+    const int r = lane & 15, g = lane >> 4;
 
     const int rx = (int)min((int64_t)BM, p.M - m0);
     const int64_t rows_w = TILED ? (p.N + 15) / 16 * 16 : p.N;
     const int rw = (int)min((int64_t)BN, rows_w - n0);
-    const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.K, (uint32_t)rx * (uint32_t)p.K);
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.codes + n0 * p.K, (uint32_t)rw * (uint32_t)p.K);
-    uint32_t off[C::kData];  // of this lane's 16 bytes at block 0; blocks of the stage: x's rows, then w's
+    // This lane's 16 bytes at block 0 of each load: x's rows in halves (every
+    // wave row's first tokens, then its last), w's rows or tiles.
+    constexpr int R = BM / WAVES_M;  // tokens of a wave
+    auto x_row = [&](int half, int l) {
+        const int j = wave + NW * l;
+        return j / (R / 16) * R + half * (R / 2) + 8 * (j % (R / 16));
+    };
+    uint32_t xo[2][C::kHalf], wo[C::kW];
 #pragma unroll
-    for (int l = 0; l < C::kData; ++l) {
-        const int blk = wave + NW * l;
-        const int row = 8 * blk + (lane >> 3);
-        if (8 * blk < BM) {
-            off[l] = (uint32_t)min(row, rx - 1) * (uint32_t)p.K + 16u * swz<8>(row, lane & 7);
-        } else if (TILED) {
-            const int b = blk - BM / 8;  // two 1 KB units per 16 rows
-            off[l] = (uint32_t)min(b >> 1, rw / 16 - 1) * 16u * (uint32_t)p.K + 1024u * (b & 1) + 16u * lane;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int l = 0; l < C::kHalf; ++l) {
+            const int row = x_row(h, l) + (lane >> 3);
+            xo[h][l] = (uint32_t)min(row, rx - 1) * (uint32_t)p.K + 16u * swz<8>(row, lane & 7);
+        }
+#pragma unroll
+    for (int l = 0; l < C::kW; ++l) {
+        const int b = wave + NW * l, row = 8 * b + (lane >> 3);
+        wo[l] = TILED ? (uint32_t)min(b >> 1, rw / 16 - 1) * 16u * (uint32_t)p.K + 1024u * (b & 1) + 16u * lane
+                      : (uint32_t)min(row, rw - 1) * (uint32_t)p.K + 16u * swz<8>(row, lane & 7);
+    }
+    const float* ssrc[C::kSL];
+    int64_t sstr[C::kSL];
+    int sdst[C::kSL];
+#pragma unroll
+    for (int l = 0; l < C::kSL; ++l) {
+        const int sj = min(wave + NW * l, C::kScaleLoads - 1);
+        if (sj < BM / 64) {
+            ssrc[l] = p.s_x + m0 + min(64 * sj + lane, rx - 1);
+            sstr[l] = p.M;
+        } else {  // lanes past BN / 128 repeat the last: all in one line
+            const int64_t nb = min(n0 / kFp8Block + min(lane, (BN - 1) / kFp8Block), (p.N - 1) / kFp8Block);
+            ssrc[l] = p.s_w + nb * p.KB;
+            sstr[l] = 1;
+        }
+        sdst[l] = STAGES * C::kCodes + 256 * sj;
+    }
+    // Blocks past the last are requested outside of empty buffers: nothing is
+    // read, the loop has no branch, and every wait is for the same number of loads.
+    const uint32_t x_bytes = (uint32_t)rx * (uint32_t)p.K, w_bytes = (uint32_t)rw * (uint32_t)p.K;
+    auto issue_x = [&](int h, int l, int kb, int to) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.K, kb < kb1 ? x_bytes : 0u);
+        dma16_buffer(xr, smem + to * C::kCodes + x_row(h, l) * kFp8Block, xo[h][l], (uint32_t)kb * 128u);
+    };
+    // load i of a block's first part: w, half of x, the steps
+    auto issue_first = [&](int i, int kb, int to, int sto) __attribute__((always_inline)) {
+        if (i < C::kW) {
+            const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.codes + n0 * p.K, kb < kb1 ? w_bytes : 0u);
+            dma16_buffer(wr, smem + to * C::kCodes + (BM / 8 + wave + NW * i) * 1024, wo[i],
+                         (uint32_t)kb * (TILED ? 2048u : 128u));
+        } else if (i < C::kW + C::kHalf) {
+            issue_x(0, i - C::kW, kb, to);
         } else {
-            off[l] = (uint32_t)min(row - BM, rw - 1) * (uint32_t)p.K + 16u * swz<8>(row - BM, lane & 7);
+            const int l = i - C::kW - C::kHalf;
+            dma4(ssrc[l] + (int64_t)min(kb, kb1 - 1) * sstr[l], smem + sdst[l] + sto * C::kScales);
         }
-    }
-    // the steps: wave j < BM / 64 those of 64 tokens, the next one the matrix's
-    const int sj = min(wave, C::kScaleLoads - 1);
-    const float* ssrc;
-    int64_t sstr;
-    if (sj < BM / 64) {
-        ssrc = p.s_x + m0 + min(64 * sj + lane, rx - 1);
-        sstr = p.M;
-    } else {
-        const int64_t nb = min(n0 / kFp8Block + lane, (p.N - 1) / kFp8Block);
-        ssrc = p.s_w + nb * p.KB;
-        sstr = 1;
-    }
-    auto issue = [&](int kb) {
-        uint8_t* base = smem + (kb % STAGES) * C::kStage;
-#pragma unroll
-        for (int l = 0; l < C::kData; ++l) {
-            const int blk = wave + NW * l;
-            const bool isx = 8 * blk < BM;
-            dma16_buffer(isx ? xr : wr, base + blk * 1024, off[l], (uint32_t)kb * (!isx && TILED ? 2048u : 128u));
-        }
-        dma4(ssrc + kb * sstr, base + C::kCodes + 256 * sj);
     };
 
     f32x4 acc[NT][MT];
@@ -304,57 +355,190 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void fp8_tile_kernel(Fp8Par
     for (int a = 0; a < NT; ++a)
 #pragma unroll
         for (int b = 0; b < MT; ++b) acc[a][b] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < p.KB) issue(s);
 
-    const int r = lane & 15, g = lane >> 4;
-    for (int kb = 0; kb < p.KB; ++kb) {
-        wait_later<C::kLPS, STAGES - 2>(min(STAGES - 2, p.KB - 1 - kb));
-        lds_barrier();  // every wave's part of block kb is there, and block kb - 1 is read
-        if (kb + STAGES - 1 < p.KB) issue(kb + STAGES - 1);
-        const uint8_t* base = smem + (kb % STAGES) * C::kStage;
+    // Fragments and steps of a block, read from its LDS buffer.
+    constexpr int LA = MT > 2 ? 2 : 1;
+    constexpr int XR = MT > 2 ? 4 : 2;
+    static_assert(MT % XR == 0, "a whole turn of the ring per block");
+    u32x4 fw[NT][2], fx[XR][2];
+    float sx[XR], sw = 0.0f;
+    const int xrow = wm * R + r, wrow = wn * (16 * NT) + r;
+    auto read_x = [&](const uint8_t* base, const uint8_t* sc, int b) __attribute__((always_inline)) {
+        const int row = xrow + 16 * b;
+        fx[b % XR][0] = *reinterpret_cast<const u32x4*>(base + row * kFp8Block + 16 * swz<8>(row, g));
+        fx[b % XR][1] = *reinterpret_cast<const u32x4*>(base + row * kFp8Block + 16 * swz<8>(row, g + 4));
+        sx[b % XR] = *reinterpret_cast<const float*>(sc + 4 * row);
+    };
+    auto read_w = [&](const uint8_t* base, int a) __attribute__((always_inline)) {
         const uint8_t* wbase = base + BM * kFp8Block;
-        const float* sbase = reinterpret_cast<const float*>(base + C::kCodes);
-        const float sw = sbase[BM + wn * (BN / WAVES_N) / kFp8Block];
-        auto frag_x = [&](int b) {
-            const int row = wm * (16 * MT) + 16 * b + r;
-            return operand<WIDE>(*reinterpret_cast<const u32x4*>(base + row * kFp8Block + 16 * swz<8>(row, g)),
-                           *reinterpret_cast<const u32x4*>(base + row * kFp8Block + 16 * swz<8>(row, g + 4)));
-        };
-        auto frag_w = [&](int a) {
-            if constexpr (TILED) {
-                const uint8_t* q = wbase + (wn * NT + a) * 2048 + 16 * lane;
-                return operand<WIDE>(*reinterpret_cast<const u32x4*>(q), *reinterpret_cast<const u32x4*>(q + 1024));
-            } else {
-                const int row = wn * (16 * NT) + 16 * a + r;
-                return operand<WIDE>(*reinterpret_cast<const u32x4*>(wbase + row * kFp8Block + 16 * swz<8>(row, g)),
-                               *reinterpret_cast<const u32x4*>(wbase + row * kFp8Block + 16 * swz<8>(row, g + 4)));
-            }
-        };
-        Operand<WIDE> fw[NT];
+        if constexpr (TILED) {
+            const uint8_t* q = wbase + (wn * NT + a) * 2048 + 16 * lane;
+            fw[a][0] = *reinterpret_cast<const u32x4*>(q);
+            fw[a][1] = *reinterpret_cast<const u32x4*>(q + 1024);
+        } else {
+            const int row = wrow + 16 * a;
+            fw[a][0] = *reinterpret_cast<const u32x4*>(wbase + row * kFp8Block + 16 * swz<8>(row, g));
+            fw[a][1] = *reinterpret_cast<const u32x4*>(wbase + row * kFp8Block + 16 * swz<8>(row, g + 4));
+        }
+    };
+    auto read_sw = [&](const uint8_t* sc) {
+        return reinterpret_cast<const float*>(sc)[BM + wn * (BN / WAVES_N) / kFp8Block];
+    };
+
+    // Block products wait in a ring for kLag steps before the vector unit
+    // takes them up, so that neither waits for the other.
+    constexpr int kLag = NT < 3 ? NT : 3, T = NT * MT;
+    static_assert(T % 4 == 0, "ring of four");
+    f32x4 d[4];
+    float c_last = 0.0f;
 #pragma unroll
-        for (int a = 0; a < NT; ++a) fw[a] = frag_w(a);
+    for (int i = 0; i < 4; ++i) d[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+
+    const uint8_t* scales = smem + STAGES * C::kCodes;
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+#pragma unroll
+        for (int i = 0; i < C::kFirst; ++i) issue_first(i, kb0 + s, s, s);
+#pragma unroll
+        for (int i = 0; i < C::kSecond; ++i) issue_x(1, i, kb0 + s, s);
+    }
+    // The loads younger than the part that a wait is for: the first part of block
+    // kb + 1 at S2 (after it the second of kb + 1, then pairs up to the first of
+    // kb + STAGES), the second part of block kb at S1 likewise.
+    constexpr int kAhead = (STAGES - 1) * (C::kFirst + C::kSecond);
+    wait_vmcnt<kAhead + C::kSecond>();
+    lds_barrier();
+#pragma unroll
+    for (int b = 0; b < LA; ++b) read_x(smem, scales, b);
+#pragma unroll
+    for (int a = 0; a < NT; ++a) read_w(smem, a);
+    sw = read_sw(scales);
+
+    constexpr int S1 = MT / 2 > LA ? MT / 2 - LA : 0, S2 = MT - LA;
+    int slot = 0, sslot = 0;  // of block kb; the steps have one buffer more, as they are read to the block's end
+    for (int kb = kb0; kb < kb1; ++kb) {
+        const uint8_t* here = smem + slot * C::kCodes;
+        const uint8_t* shere = scales + sslot * C::kScales;
+        const int freed = slot, sfree = sslot == 0 ? STAGES : sslot - 1;
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        sslot = sslot == STAGES ? 0 : sslot + 1;
+        const uint8_t* next = smem + slot * C::kCodes;
+        const uint8_t* snext = scales + sslot * C::kScales;
+        float sw_next = 0.0f;
+        Operand<WIDE> w[NT];
 #pragma unroll
         for (int b = 0; b < MT; ++b) {
-            const Operand<WIDE> fx = frag_x(b);
-            const float c = sbase[wm * (16 * MT) + 16 * b + r] * sw;
+            if (b == S1) {  // the second half of block kb has landed; its matrix rows and first half are read
+                wait_vmcnt<kAhead>();
+                lds_barrier();
+            }
+            if (b == S2) {  // the first part of block kb + 1 has landed; all of block kb is read
+                wait_vmcnt<kAhead>();
+                lds_barrier();
+                sw_next = read_sw(snext);
+            }
+            const Operand<WIDE> x = operand<WIDE>(fx[b % XR][0], fx[b % XR][1]);
+            const float c = sx[b % XR] * sw;
+            if (b < MT - LA) read_x(here, shere, b + LA);
+            else read_x(next, snext, b + LA - MT);
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
-                const f32x4 d = block_product<WIDE>(fw[a], fx);
+                if (b == 0) w[a] = operand<WIDE>(fw[a][0], fw[a][1]);
+                const int t = b * NT + a, u = (t + T - kLag) % T;
+                d[t & 3] = block_product<WIDE>(w[a], x);
+                constexpr int n1 = (S2 - S1) * NT, n2 = (MT - S2) * NT;
+                if (b >= S1 && b < S2) {
+                    const int q = t - S1 * NT;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[a][b][i] = __builtin_fmaf(d[i], c, acc[a][b][i]);
+                    for (int i = q * C::kFirst / n1; i < (q + 1) * C::kFirst / n1; ++i)
+                        issue_first(i, kb + STAGES, freed, sfree);
+                } else if (b >= S2) {
+                    const int q = t - S2 * NT;
+#pragma unroll
+                    for (int i = q * C::kSecond / n2; i < (q + 1) * C::kSecond / n2; ++i)
+                        issue_x(1, i, kb + STAGES, freed);
+                }
+                if (b == MT - 1) read_w(next, a);
+                const float cu = a < kLag ? c_last : c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4& v = acc[u % NT][u / NT];
+                    v[i] = __builtin_fmaf(d[u & 3][i], cu, v[i]);
+                }
             }
+            c_last = c;
+            if constexpr (!WIDE) {
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads,
+                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // vector instructions
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        sw = sw_next;
     }
+    wait_vmcnt<0>();  // no load into LDS outlives the workgroup
+#pragma unroll
+    for (int u = T - kLag; u < T; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4& v = acc[u % NT][u / NT];
+            v[i] = __builtin_fmaf(d[u & 3][i], c_last, v[i]);
+        }
 #pragma unroll
     for (int b = 0; b < MT; ++b) {
-        const int64_t m = m0 + wm * (16 * MT) + 16 * b + r;
+        const int64_t m = m0 + wm * R + 16 * b + r;
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
             const int64_t n = n0 + wn * (16 * NT) + 16 * a + 4 * g;
-            if (m < p.M && n < p.N) store4(p, m, n, acc[a][b]);
+            if (m < p.M && n < p.N) store4(out, m, n, acc[a][b]);
         }
+    }
+}
+
+// Tile t of tiles_m x tiles_n, in supertiles of 4 token tiles: workgroups that
+// follow one another, and so the XCD's that share an L2, read the same rows.
+__device__ __forceinline__ void tile_at(int64_t t, int tiles_m, int tiles_n, int64_t& tm, int64_t& tn) {
+    const int64_t per = 4 * (int64_t)tiles_n;
+    const int64_t st = t / per, u = t - st * per;
+    const int64_t h = min((int64_t)4, tiles_m - 4 * st);
+    tm = 4 * st + u % h;
+    tn = u / h;
+}
+
+// Tiles of kind A, then those of kind B for the matrix rows from n1 on.
+template <class A, class B, bool TILED, bool WIDE>
+__global__ __launch_bounds__(64 * A::kNW) void fp8_tile_kernel(Fp8Params p) {
+    static_assert(A::kNW == B::kNW, "one size of workgroup");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[A::kLds > B::kLds ? A::kLds : B::kLds];
+    const int64_t first = (int64_t)p.tiles_m * p.tiles_n * p.parts;
+    int64_t tm, tn;
+    if (blockIdx.x < first) {
+        const int64_t w = xcd_run(blockIdx.x, first), tiles = (int64_t)p.tiles_m * p.tiles_n;
+        const int part = (int)(w / tiles);
+        tile_at(w - part * tiles, p.tiles_m, p.tiles_n, tm, tn);
+        const int64_t ld = (p.N + 3) / 4 * 4;
+        const Out o = p.parts == 1 ? output_of(p) : Out{p.sums + part * p.M * ld, 0, ld, ld, true};
+        fp8_tile<A, TILED, WIDE>(p, smem, tm * A::BM, tn * A::BN, (int)((int64_t)p.KB * part / p.parts),
+                                 (int)((int64_t)p.KB * (part + 1) / p.parts), o);
+    } else if constexpr (!std::is_same<A, B>::value) {
+        tile_at(xcd_run(blockIdx.x - first, gridDim.x - first), p.tiles_m2, p.tiles_n2, tm, tn);
+        fp8_tile<B, TILED, WIDE>(p, smem, tm * B::BM, p.n1 + tn * B::BN, 0, p.KB, output_of(p));
+    }
+}
+
+// The sums of the parts of k, added in their order.
+__global__ __launch_bounds__(kThreads) void fp8_join_kernel(Fp8Params p) {
+    const int64_t ld4 = (p.N + 3) / 4, chunks = p.M * ld4;
+    const Out o = output_of(p);
+    const f32x4* s = reinterpret_cast<const f32x4*>(p.sums);
+    for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < chunks; c += (int64_t)gridDim.x * kThreads) {
+        f32x4 v = s[c];
+        for (int q = 1; q < p.parts; ++q) v += s[q * chunks + c];
+        const int64_t m = c / ld4;
+        store4(o, m, 4 * (c - m * ld4), v);
     }
 }
 
@@ -366,21 +550,134 @@ hipError_t run_stream(const Fp8Params& p, bool t16, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, bool WIDE>
-hipError_t run_tile(Fp8Params p, bool t16, hipStream_t st) {
-    p.tiles_m = (int)((p.M + BM - 1) / BM);
-    p.tiles_n = (int)((p.N + BN - 1) / BN);
-    const uint32_t grid = (uint32_t)((int64_t)p.tiles_m * p.tiles_n);
-    constexpr int T = 64 * WAVES_M * WAVES_N;
-    if (t16) fp8_tile_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, true, WIDE><<<grid, T, 0, st>>>(p);
-    else fp8_tile_kernel<BM, BN, WAVES_M, WAVES_N, STAGES, false, WIDE><<<grid, T, 0, st>>>(p);
+// cols: columns of tiles of kind A (all of them where that is enough).
+template <class A, class B, bool WIDE>
+hipError_t run_tiles(Fp8Params p, bool t16, hipStream_t st, int64_t cols, int parts) {
+    p.tiles_m = (int)((p.M + A::BM - 1) / A::BM);
+    p.tiles_n = (int)((p.N + A::BN - 1) / A::BN);
+    p.tiles_m2 = p.tiles_n2 = 0;
+    if (cols < p.tiles_n) {
+        p.tiles_n = (int)cols;
+        p.n1 = cols * A::BN;
+        p.tiles_m2 = (int)((p.M + B::BM - 1) / B::BM);
+        p.tiles_n2 = (int)((p.N - p.n1 + B::BN - 1) / B::BN);
+    }
+    p.parts = parts;
+    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n * parts + (int64_t)p.tiles_m2 * p.tiles_n2;
+    if (t16) fp8_tile_kernel<A, B, true, WIDE><<<(uint32_t)grid, 64 * A::kNW, 0, st>>>(p);
+    else fp8_tile_kernel<A, B, false, WIDE><<<(uint32_t)grid, 64 * A::kNW, 0, st>>>(p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || parts == 1) return e;
+    const int64_t chunks = p.M * ((p.N + 3) / 4), want = (chunks + kThreads - 1) / kThreads;
+    fp8_join_kernel<<<(uint32_t)(want < 4096 ? want : 4096), kThreads, 0, st>>>(p);
     return hipGetLastError();
+}
+
+typedef Fp8Tile<256, 256, 2, 4, 2> TileXL;
+typedef Fp8Tile<256, 128, 4, 2, 2> TileL;
+typedef Fp8Tile<128, 128, 2, 4, 2> TileM;
+typedef Fp8Tile<64, 64, 2, 2, 4> TileS;
+
+// Which kernel runs goes by what each is expected to take, in us, from the
+// sizes alone.  A tile costs `step` per block of k where its CU has one, `more`
+// for each further one that shares the CU or comes after it (measured with all
+// CUs at work: clocks are lower then), and `start` per launch.  Taken at
+// 4096 x 4096 x 16384 (bf16 y: XL 214 us, L 246, M 277, S 420), 128 x 4096 x 4096
+// (43, 28, 21, 15) and the shapes named below.
+enum TileKind { kS, kM, kL, kXL };
+struct TileCost {
+    int bm, bn;
+    double start, step, more;
+};
+constexpr TileCost kNarrow[] = {{64, 64, 4.5, 0.31, 0.20}, {128, 128, 5, 0.53, 0.54}, {256, 128, 6, 0.90, 0.95},
+                                {256, 256, 8, 1.50, 1.60}};
+constexpr TileCost kWide[] = {{64, 64, 4.5, 0.47, 0.33}, {128, 128, 5, 0.98, 1.08}, {256, 128, 6, 1.70, 1.85}};
+
+struct Fp8Plan {
+    bool stream;
+    int kind, parts;
+    int64_t cols;  // kXL: columns of tiles before kL takes over
+    double us;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+double tiles_us(const TileCost& t, int64_t tiles, double blocks) {
+    const int64_t c = ceil_div(tiles, kCUs);
+    return blocks * (t.step + (double)(c - 1) * t.more);
+}
+
+// Streams read the matrix once per 32 tokens and both operands per workgroup's
+// outputs (16 or 32 matrix rows x 32 tokens): 4 us, then 6.5 TB/s of the one and
+// 16 TB/s of the other, or 66 bytes per ns of a CU where few have work (64 x 4096
+// x 4096 8.0 us, 64 x 11008 x 4096 21.3, 32 x 11008 x 4096 17).
+bool stream_narrow(int64_t m, int64_t n) { return ceil_div(n, 16) * ceil_div(m, 32) <= kCUs; }
+
+double stream_us(int64_t m, int64_t n, int64_t k) {
+    const double nk = (double)n * (double)k;
+    if (m <= 16) return 4 + nk / 6.5e6;
+    const int rows = stream_narrow(m, n) ? 16 : 32;
+    const double per = (double)(rows + 32) * (double)k, wgs = (double)ceil_div(n, rows) * (double)ceil_div(m, 32);
+    const double all = nk / 6.5e6 + wgs * per / 16e6, one = (double)ceil_div((int64_t)wgs, kCUs) * per / 66e3;
+    return 4 + (all > one ? all : one);
+}
+
+// Parts of k: their fp32 sums are written and read again, by a second launch
+// (300 x 4096 x 11008: M whole 52.7 us, in 2 parts 35.8, in 5 34.3; L in 4 34.7).
+double join_us(int64_t m, int64_t n, int parts) {
+    return parts == 1 ? 0.0 : 3.5 + 4.0 * parts * (double)m * (double)n / 3.5e6;
+}
+
+Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int yt) {
+    Fp8Plan best = {true, 0, 1, 0, stream_us(m, n, k)};
+    if (m <= 16) return best;
+    const int64_t kb = k / kFp8Block;
+    const TileCost* cost = yt == 0 ? kWide : kNarrow;
+    for (int kind = kS; kind <= (yt == 0 ? kL : kXL); ++kind) {
+        const TileCost& t = cost[kind];
+        const int64_t tiles = ceil_div(m, t.bm) * ceil_div(n, t.bn);
+        for (int parts = 1; parts <= kMaxParts && parts <= kb; ++parts) {
+            if (parts > 1 && tiles * (parts - 1) >= 2 * kCUs) break;  // CUs enough without
+            const double us = t.start + tiles_us(t, tiles * parts, (double)ceil_div(kb, parts)) + join_us(m, n, parts);
+            if (us < best.us) best = {false, kind, parts, n, us};
+        }
+    }
+    // whole rounds of XL, the rest of the matrix in L (2048 x 11008 x 4096: XL
+    // 118 us, L 106, 32 columns of XL and 22 of L 99)
+    if (yt != 0) {
+        const int64_t tm = ceil_div(m, cost[kXL].bm), tn = ceil_div(n, cost[kXL].bn), rounds = tm * tn / kCUs;
+        const int64_t cols = rounds * kCUs / tm;
+        if (rounds >= 1 && cols < tn) {
+            const int64_t rest = ceil_div(m, cost[kL].bm) * ceil_div(n - cols * cost[kXL].bn, cost[kL].bn);
+            const double us = cost[kXL].start + tiles_us(cost[kXL], tm * cols, (double)kb) +
+                              (double)kb * (double)ceil_div(rest, kCUs) * cost[kL].more;
+            if (us < best.us) best = {false, kXL, 1, cols, us};
+        }
+    }
+    return best;
+}
+
+template <bool WIDE>
+hipError_t run_plan(const Fp8Params& p, bool t16, const Fp8Plan& plan, hipStream_t st) {
+    switch (plan.kind) {
+        case kS: return run_tiles<TileS, TileS, WIDE>(p, t16, st, p.N, plan.parts);
+        case kM: return run_tiles<TileM, TileM, WIDE>(p, t16, st, p.N, plan.parts);
+        case kL: return run_tiles<TileL, TileL, WIDE>(p, t16, st, p.N, plan.parts);
+        default: break;
+    }
+    if constexpr (WIDE) return hipErrorInvalidValue;  // no plan of fp32 outputs has it
+    else return run_tiles<TileXL, TileL, false>(p, t16, st, plan.cols, plan.parts);
 }
 
 }  // namespace
 
+size_t fp8_workspace(int64_t m, int64_t n, int64_t k, int yt) {
+    const Fp8Plan plan = plan_fp8(m, n, k, yt);
+    return plan.parts == 1 ? 0 : (size_t)plan.parts * (size_t)m * (size_t)((n + 3) / 4 * 4) * sizeof(float);
+}
+
 hipError_t launch_qgemm_fp8(const Fp8GemmArgs& a, hipStream_t st) {
-    Fp8Params p;
+    Fp8Params p = {};
     p.codes = a.codes;
     p.s_w = a.s_w;
     p.x = a.x;
@@ -391,11 +688,18 @@ hipError_t launch_qgemm_fp8(const Fp8GemmArgs& a, hipStream_t st) {
     p.KB = (int)(a.k / kFp8Block);
     p.y = a.y;
     p.yt = a.yt;
-    p.tiles_m = p.tiles_n = 0;
-    if (a.m <= 16) return run_stream<1, 1, true, 8, 4>(p, a.t16, st);
-    if (a.m <= 64) return run_stream<4, 1, true, 8, 2>(p, a.t16, st);
-    if (a.yt == 0) return run_tile<256, 256, 2, 4, 2, true>(p, a.t16, st);
-    return run_tile<256, 256, 2, 4, 2, false>(p, a.t16, st);
+    p.sums = static_cast<float*>(a.ws);
+    const Fp8Plan plan = plan_fp8(a.m, a.n, a.k, a.yt);
+    if (!plan.stream) return a.yt == 0 ? run_plan<true>(p, a.t16, plan, st) : run_plan<false>(p, a.t16, plan, st);
+    // Streams: 32 matrix rows per workgroup where 16 give more than two to a CU
+    // (16 x 22016 x 4096: 23.6 -> 18.7 us in tiles; 16 x 4096 x 4096: 5.4 against 5.8)
+    const int64_t tiles = ceil_div(a.n, 16);
+    if (a.m <= 16) {
+        if (tiles <= 4 * kCUs) return run_stream<1, 1, true, 8, 2>(p, a.t16, st);
+        return run_stream<1, 2, true, 8, 1>(p, a.t16, st);
+    }
+    if (stream_narrow(a.m, a.n)) return run_stream<2, 1, true, 8, 2>(p, a.t16, st);
+    return run_stream<2, 2, true, 8, 1>(p, a.t16, st);
 }
 
 }  // namespace qg

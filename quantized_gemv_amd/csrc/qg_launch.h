@@ -248,7 +248,9 @@ struct Fp8GemmArgs {
     int64_t m, n, k;
     void* y;
     int yt;
+    void* ws;              // fp8_workspace bytes
 };
+size_t fp8_workspace(int64_t m, int64_t n, int64_t k, int yt);
 hipError_t launch_qgemm_fp8(const Fp8GemmArgs& a, hipStream_t st);
 
 int device_cu_count();

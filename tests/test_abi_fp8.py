@@ -10,7 +10,7 @@ A, U = 1 << 40, (1 << 40) + 1  # a 16-B aligned fake address, and a misaligned o
 FAR = [A + (j << 44) for j in range(8)]  # addresses far enough apart for every size here
 needs_no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0,
                                   reason="passes fake device addresses; runs where no GPU is visible")
-HIP, NULLPTR, SHAPE, ALIGN, ARG = 6, 1, 2, 3, 4
+HIP, NULLPTR, SHAPE, ALIGN, ARG, WORKSPACE = 6, 1, 2, 3, 4, 5
 
 
 @pytest.fixture(scope="module")
@@ -121,13 +121,13 @@ def test_validation_swiglu_and_quantizers(qg):
 
 @needs_no_gpu
 def test_validation_product(qg):
-    def product(x=FAR[0], s_x=FAR[1], m=4, y=FAR[2], yt=1, **kw):
+    def product(x=FAR[0], s_x=FAR[1], m=4, y=FAR[2], yt=1, ws=None, nws=0, **kw):
         a = dict(fmt=qg.QG_WFMT_FP8, n=130, k=256, codes=FAR[3], scale=FAR[4])
         a.update(kw)
         w = qg.CWeight(a["fmt"], 0, a["n"], a["k"], a["codes"], None, a["scale"], None, None)
-        return qg.lib().qg_qgemm_fp8(ctypes.byref(w), x, s_x, m, y, yt, None)
+        return qg.lib().qg_qgemm_fp8(ctypes.byref(w), x, s_x, m, y, yt, ws, nws, None)
 
-    assert qg.lib().qg_qgemm_fp8(None, A, A, 4, A, 1, None) == NULLPTR
+    assert qg.lib().qg_qgemm_fp8(None, A, A, 4, A, 1, None, 0, None) == NULLPTR
     for name in ("x", "s_x", "y", "codes", "scale"):
         assert product(**{name: None}) == NULLPTR
     for fmt in (qg.QG_WFMT_INT8, qg.QG_WFMT_INT8_T16, 9, -1):
@@ -144,6 +144,18 @@ def test_validation_product(qg):
     # the rows that pad the last tile are the matrix's, too
     assert product(y=FAR[3] + 130 * 256) == HIP and product(y=FAR[3] + 130 * 256, fmt=qg.QG_WFMT_FP8_T16) == ARG
     assert product() == HIP and product(fmt=qg.QG_WFMT_FP8_T16, yt=0) == HIP
+    # few tiles and a long k: parts of k meet in the workspace
+    f = qg.lib().qg_qgemm_fp8_workspace_bytes
+    big = dict(m=300, n=4096, k=11008)
+    need = f(300, 4096, 11008, 1)
+    assert need >= 2 * 300 * 4096 * 4 and need % (300 * 4096 * 4) == 0
+    assert product(**big) == WORKSPACE and product(ws=FAR[5], nws=need - 1, **big) == WORKSPACE
+    assert product(ws=FAR[5] + 8, nws=need, **big) == ALIGN
+    for name, at in (("x", 0), ("s_x", 1), ("y", 2), ("codes", 3), ("scale", 4)):
+        assert product(ws=FAR[at], nws=need, **big) == ARG, name
+    assert product(ws=FAR[5], nws=need, **big) == HIP
+    assert f(1, 4096, 4096, 1) == 0 and f(4096, 11008, 4096, 1) == 0
+    assert f(300, 4096, 11007, 1) == 0 and f(0, 4096, 11008, 1) == 0 and f(300, 4096, 11008, 2) == 0
 
 
 @needs_no_gpu

@@ -115,6 +115,67 @@ def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
     assert np.array_equal(host(run(qg, W, e4(x), dev(s_x), torch.bfloat16)), f32_to_bf16_rne(y))
 
 
+# every kind of tile, in parts of k and not, and two kinds in one launch; ends
+# inside tiles in both directions
+LARGE = [(300, 4096, 11008), (2048, 512, 8192), (700, 4100, 1152), (1000, 1003, 8192), (4096, 4352, 128), (4100, 4611, 256),
+         (2048, 2050, 4096), (513, 11008, 640), (9000, 128, 384), (130, 20001, 256), (4096, 8192, 384)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_large_exact(qg, m, n, k):
+    """Whole codes again; the reference is the fp64 product on the GPU, exact here."""
+    torch.manual_seed(m + n + k)
+    x = torch.randint(-4, 5, (m, k), device="cuda").float().to(E4)
+    w = torch.randint(-4, 5, (n, k), device="cuda").float().to(E4)
+    s_x = 2.0 ** torch.randint(-1, 2, (k // 128, m), device="cuda").float()
+    s_w = 2.0 ** torch.randint(-1, 2, (-(-n // 128), k // 128), device="cuda").float()
+    xs = x.double().view(m, k // 128, 128) * s_x.t().double()[:, :, None]
+    ws = w.double().view(n, k // 128, 128) * s_w.double().repeat_interleave(128, 0)[:n, :, None]
+    ref = torch.matmul(xs.view(m, k), ws.view(n, k).t().contiguous())
+    del xs, ws
+    assert 16 * 4 * 4 * k < 2 ** 24 * 4  # |terms| <= 16, times steps of 1/4 .. 4, in units of 1/4
+    W = qg.QWeight(qg.QG_WFMT_FP8, n, k, w, s_w)
+    for tiled in (False, True):
+        note("large m=%d n=%d k=%d tiled=%s" % (m, n, k, tiled))
+        L = qg.tiled16(W) if tiled else W
+        assert torch.equal(run(qg, L, x, s_x), ref.float())
+        assert torch.equal(run(qg, L, x, s_x, torch.bfloat16), ref.float().bfloat16())
+
+
+def test_workspaces(qg):
+    """A workspace of the caller's, whatever it holds; an object's own on another
+    stream; too small a one."""
+    note("workspaces")
+    m, n, k = 300, 4096, 11008
+    x = torch.randint(0, 0x48, (m, k), dtype=torch.uint8, device="cuda").view(E4)
+    W = qg.QWeight(qg.QG_WFMT_FP8, n, k, torch.randint(0, 0x48, (n, k), dtype=torch.uint8, device="cuda").view(E4),
+                   torch.rand(n // 128, k // 128, device="cuda"))
+    s_x = torch.rand(k // 128, m, device="cuda")
+    y = qg.qgemm_fp8(W, x, s_x, y_dtype=torch.float32)
+    need = qg.lib().qg_qgemm_fp8_workspace_bytes(m, n, k, qg.QG_F32)
+    assert need > 0
+    for fill in (0, 255):
+        full, ws = guarded(need, torch.uint8)
+        ws.fill_(fill)
+        assert torch.equal(qg.qgemm_fp8(W, x, s_x, y_dtype=torch.float32, ws=ws), y)
+        assert canaries_intact(full, need)
+    with pytest.raises(qg.QgError):
+        qg.qgemm_fp8(W, x, s_x, y_dtype=torch.float32, ws=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = qg.QgemmFp8Launch(W, x, s_x, y_dtype=torch.float32)
+    out = a.y
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            a.launch()
+    del a  # its workspace must not be given out while the side stream works
+    junk = [torch.full((need // 4,), float("nan"), device="cuda") for _ in range(4)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(out, y)
+    del junk
+
+
 @pytest.mark.parametrize("m", [1, 16, 61, 130, 300])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_all_codes(qg, m, tiled):
@@ -172,51 +233,65 @@ def test_large_steps_and_small_ones(qg):
             assert np.all(np.abs(y - ref) <= 265 * HALF * size)
 
 
+def whole_codes(*shape):
+    """Codes of -2, -1, 0, 1 and 2, made in slices."""
+    table = torch.tensor([-2.0, -1.0, 0.0, 1.0, 2.0], device="cuda").to(E4).view(torch.uint8)
+    out = torch.empty(shape, dtype=torch.uint8, device="cuda")
+    for rows in out.view(-1, shape[-1]).split(8192):
+        rows.copy_(table[torch.randint(0, 5, rows.shape, device="cuda")])
+    return out.view(E4)
+
+
+def rows_of(t, at):
+    return t.view(torch.uint8)[at:].contiguous().view(E4)
+
+
 def test_far_offsets(qg):
-    """Matrices, activations and outputs past 4 GiB."""
+    """Matrices, activations and outputs past 4 GiB, against their last rows
+    alone. Whole codes and steps of 1 and 1/2: sums below 2^18 in halves, so
+    exact whichever kernel adds them."""
     note("far offsets")
+    step = lambda *s: 0.5 + 0.5 * torch.randint(0, 2, s, device="cuda").float()
     k = 65536
     n = (1 << 32) // k + 300
-    w = torch.randint(0, 0x48, (n, k), dtype=torch.uint8, device="cuda")
-    s_w = torch.rand(-(-n // 128), k // 128, device="cuda")
-    x = torch.randint(0, 0x48, (20, k), dtype=torch.uint8, device="cuda").view(E4)
-    s_x = torch.rand(k // 128, 20, device="cuda")
+    at = 65408  # 128 rows of step before 4 GiB
+    w, s_w = whole_codes(n, k), step(-(-n // 128), k // 128)
+    x, s_x = whole_codes(20, k), step(k // 128, 20)
     for tiled in (False, True):
-        W = qg.QWeight(qg.QG_WFMT_FP8, n, k, w.view(E4), s_w)
-        W = qg.tiled16(W) if tiled else W
+        W = qg.QWeight(qg.QG_WFMT_FP8, n, k, w, s_w)
+        part = qg.QWeight(qg.QG_WFMT_FP8, n - at, k, rows_of(w, at), s_w[at // 128:].contiguous())
+        if tiled:
+            W, part = qg.tiled16(W), qg.tiled16(part)
         for rows in (1, 20):
-            xs, ss = x[:rows].contiguous(), s_x[:, :rows].contiguous()
+            xs, ss = rows_of(x, 20 - rows), s_x[:, 20 - rows:].contiguous()
             y = qg.qgemm_fp8(W, xs, ss, y_dtype=torch.float32)
-            part = qg.QWeight(qg.QG_WFMT_FP8, n - 65408, k, w[65408:].contiguous().view(E4), s_w[511:].contiguous())
-            part = qg.tiled16(part) if tiled else part
-            assert torch.equal(y[:, 65408:], qg.qgemm_fp8(part, xs, ss, y_dtype=torch.float32))
+            assert torch.equal(y[:, at:], qg.qgemm_fp8(part, xs, ss, y_dtype=torch.float32))
+            ref = torch.zeros(rows, n - at, dtype=torch.float64, device="cuda")
+            for b in range(k // 128):
+                cols = slice(128 * b, 128 * b + 128)
+                rows_step = s_w[at // 128:, b].double().repeat_interleave(128)[:n - at]
+                ref += (xs[:, cols].double() @ part_cols(w, at, cols).t().contiguous()) * ss[b].double()[:, None] * rows_step
+            assert torch.equal(y[:, at:], ref.float())
     # many tokens: the matrix as activations
-    W = qg.QWeight(qg.QG_WFMT_FP8, 20, k, x, torch.rand(1, k // 128, device="cuda"))
-    sx = torch.rand(k // 128, n, device="cuda")
-    y = qg.qgemm_fp8(W, w.view(E4), sx, y_dtype=torch.float32)
-    at = n // 256 * 256 - 256  # whole tiles of the same kernel
-    z = qg.qgemm_fp8(W, w[at:].contiguous().view(E4), sx[:, at:].contiguous(), y_dtype=torch.float32)
-    ref = torch.zeros(n - at, 20, dtype=torch.float64, device="cuda")
-    size = torch.zeros_like(ref)
-    for b in range(k // 128):
-        c = sx[b, at:].double()[:, None] * W.scale[0, b].double()
-        cols = slice(128 * b, 128 * b + 128)
-        t = c * (w[at:, cols].contiguous().view(E4).double() @ x[:, cols].double().t().contiguous())
-        ref += t
-        size += t.abs()  # no code here is negative
-    bound = (263 + k // 128) * HALF * size
-    assert bool(((y[at:].double() - ref).abs() <= bound).all()) and bool(((z.double() - ref).abs() <= bound).all())
+    W = qg.QWeight(qg.QG_WFMT_FP8, 20, k, x, step(1, k // 128))
+    sx = step(k // 128, n)
+    for dt in (torch.float32, torch.bfloat16):
+        y = qg.qgemm_fp8(W, w, sx, y_dtype=dt)
+        assert torch.equal(y[at:], qg.qgemm_fp8(W, rows_of(w, at), sx[:, at:].contiguous(), y_dtype=dt))
     del w, W, y
     # outputs past 4 GiB
-    m, n = 70000, 20000
-    xs = torch.randint(0, 0x48, (m, 128), dtype=torch.uint8, device="cuda").view(E4)
-    W = qg.QWeight(qg.QG_WFMT_FP8, n, 128, torch.randint(0, 0x48, (n, 128), dtype=torch.uint8, device="cuda").view(E4),
-                   torch.rand(-(-n // 128), 1, device="cuda"))
-    sx = torch.rand(1, m, device="cuda")
-    y = qg.qgemm_fp8(W, xs, sx, y_dtype=torch.bfloat16)
-    at = m // 256 * 256 - 512
-    z = qg.qgemm_fp8(W, xs[at:].contiguous(), sx[:, at:].contiguous(), y_dtype=torch.bfloat16)
-    assert torch.equal(y[at:], z)
+    m, n = 120000, 20000
+    xs, sx = whole_codes(m, 128), step(1, m)
+    W = qg.QWeight(qg.QG_WFMT_FP8, n, 128, whole_codes(n, 128), step(-(-n // 128), 1))
+    for dt in (torch.float32, torch.bfloat16):
+        y = qg.qgemm_fp8(W, xs, sx, y_dtype=dt)
+        for at in (m - 700, 53600):  # 4 GiB of bf16 end in row 107374, of fp32 in row 53687
+            assert torch.equal(y[at:at + 700], qg.qgemm_fp8(W, rows_of(xs, at)[:700], sx[:, at:at + 700].contiguous(), y_dtype=dt))
+        del y
+
+
+def part_cols(w, at, cols):
+    return w.view(torch.uint8)[at:, cols].contiguous().view(E4).double()
 
 
 def test_two_streams_and_graphs(qg):
