@@ -1261,8 +1261,12 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor = None, s: torch.Tensor = None
     columns (qg_quantize_fp8). Returns (q float8_e4m3fn, s [cols/128][rows])."""
     _dev(x, "x", (torch.float32, torch.bfloat16))
     rows, cols = _rows_cols(x, "x")
-    q = _shaped(q, "q", (rows, cols), torch.float8_e4m3fn, x)
-    s = _shaped(s, "s", (cols // QG_FP8_BLOCK, rows), torch.float32, x)
+    # torch.empty_like and sizes that are no tuple take half the host time
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn) if q is None else _shaped(q, "q", x.shape, torch.float8_e4m3fn, x)
+    if s is None:
+        s = torch.empty(cols // QG_FP8_BLOCK, rows, dtype=torch.float32, device=x.device)
+    else:
+        _shaped(s, "s", (cols // QG_FP8_BLOCK, rows), torch.float32, x)
     _call("qg_quantize_fp8", x, x.data_ptr(), _xt(x), rows, cols, q.data_ptr(), s.data_ptr())
     return q, s
 

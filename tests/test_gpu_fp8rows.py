@@ -66,7 +66,8 @@ def check_int8(y32, q, s):
 
 # lanes per row: 16, 64, 256 and more; ends inside a chunk of lanes; one row to many
 NORMS = [(1, 8), (3, 128), (17, 120), (5, 136), (16, 512), (4, 520), (33, 1024), (1, 4096), (7, 4104), (130, 5120),
-         (2, 8192), (3, 11008), (1, 16384), (2, 32768), (2, 32760), (1031, 256), (515, 2048)]
+         (2, 8192), (3, 11008), (1, 16384), (2, 24320), (2, 32768), (2, 32760), (1031, 256), (515, 2048), (300, 4096), (257, 6016),
+         (258, 8192), (259, 11008), (261, 16376), (257, 24576), (257, 28672)]
 
 
 @pytest.mark.parametrize("m,k", NORMS)
