@@ -946,8 +946,8 @@ qg_status qg_swiglu(const void* x, int32_t xt, int64_t rows, int64_t n, int32_t 
  * x   : [m][k] e4m3 codes; s_x: [k/128][m] (qg_quantize_fp8, qg_rms_norm,
  *       qg_swiglu).
  * y   : [m][n] of type yt (QG_F32 or QG_BF16).
- * k % 128 == 0, 128 <= k <= QG_BATCH_MAX_K; 1 <= m < 2^30; 1 <= n < 2^26;
- * m * k and n * k <= 2^40, m * n <= 2^38.  codes, x and y 16-B aligned, the steps
+ * k % 128 == 0, 128 <= k <= QG_BATCH_MAX_K; 1 <= m < 2^28; 1 <= n < 2^26;
+ * m * k and n * k <= 2^40, m * n <= 2^36.  codes, x and y 16-B aligned, the steps
  * 4-B.  y and ws must not overlap an input or each other (QG_ERR_ARG).
  * ws  : qg_qgemm_fp8_workspace_bytes(m, n, k, yt) bytes, 16-B aligned (may be
  *       NULL when that is 0: the fp32 sums of parts of k, at most 8 m n values,

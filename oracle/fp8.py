@@ -88,11 +88,11 @@ def swiglu(x):
         return x[:, :n] / (1.0 + np.exp(-x[:, :n])) * x[:, n:]
 
 
-def product(x, s_x, codes, scale):
+def product(x, s_x, codes, scale, cut=True):
     """[m][n] in fp64: y; the sum of the terms' absolute values; and the sum over
     every eight consecutive k of the largest power of two that is no larger than
     a product of two binades there, 2^(ex + ew) of nonzero codes (what a matrix
-    instruction that aligns eight products cuts them against)."""
+    instruction that aligns eight products cuts them against; zeros without cut)."""
     xv, wv = decode(x), decode(codes)
     y = np.zeros((xv.shape[0], wv.shape[0]))
     size, top = np.zeros_like(y), np.zeros_like(y)
@@ -104,7 +104,7 @@ def product(x, s_x, codes, scale):
         c = np.asarray(s_x[b], np.float64)[:, None] * np.asarray(scale, np.float64)[rows, b][None, :]
         y += c * (xv[:, at] @ wv[:, at].T)
         size += np.abs(c) * (np.abs(xv[:, at]) @ np.abs(wv[:, at]).T)
-        for j in range(BLOCK * b, BLOCK * (b + 1), 8):
+        for j in range(BLOCK * b, BLOCK * (b + 1), 8) if cut else ():
             big = np.zeros_like(y)
             for i in range(j, j + 8):
                 np.maximum(big, xe[:, i, None] * we[None, :, i], out=big)

@@ -117,8 +117,8 @@ qg_status check_rows(const qg::RowArgs& a, int64_t per, int64_t max_k) {
 
 qg_status check_fp8_sizes(int64_t m, int64_t n, int64_t k) {
     if (k < QG_FP8_BLOCK || k % QG_FP8_BLOCK != 0 || k > QG_BATCH_MAX_K) return QG_ERR_SHAPE;
-    if (m < 1 || m >= ((int64_t)1 << 30) || n < 1 || n >= ((int64_t)1 << 26)) return QG_ERR_SHAPE;
-    return fits(m, k) && fits(n, k) && fits(m, 4 * n) ? QG_OK : QG_ERR_SHAPE;
+    if (m < 1 || m >= ((int64_t)1 << 28) || n < 1 || n >= ((int64_t)1 << 26)) return QG_ERR_SHAPE;
+    return fits(m, k) && fits(n, k) && fits(m, 16 * n) ? QG_OK : QG_ERR_SHAPE;
 }
 
 // A row plan as the products read it.

@@ -23,6 +23,8 @@
 // Elsewhere, and for every fp32 output, the codes are widened to bf16, which
 // holds every e4m3 value, and four v_mfma_f32_16x16x32_bf16 add exact products
 // in fp32 (1.2e-8 on the same values).
+#include <cmath>
+
 #include "qg_fp8.h"
 #include "qg_gemm.h"
 #include "qg_launch.h"
@@ -35,6 +37,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int64_t kCUs = 256;  // MI355X
 constexpr int kMaxParts = 8;  // of k
+constexpr int64_t kStreamTokens = 1 << 20;  // a stream's grid stays below 2^16 along the tokens
+constexpr int64_t kMaxGroups = 1 << 23;     // and any launch below 2^32 threads
 
 struct Fp8Params {
     const uint8_t* codes;
@@ -134,14 +138,29 @@ __device__ __forceinline__ Out output_of(const Fp8Params& p) { return {p.y, p.yt
 // ------------------------------------------------------------------ few tokens
 // The time goes into reading the matrix once.  A workgroup multiplies 16 RT
 // matrix rows with 16 MT tokens; its NW waves take the blocks of k in turn, U
-// of them requested ahead, and their sums meet in LDS in wave order.  Blocks
+// of them requested ahead, and their sums meet in LDS in wave order.  Rows are
+// requested in whole lines, eight lanes to the 128 bytes of each, and pass
+// through the wave's own LDS into the order of the matrix instruction (requested
+// in that order, 16 bytes here and there: 16 x 22016 x 4096 row-major 22.5 against
+// 19.0 us, 64 x 11008 x 4096 in tiles 21.5 against 17.4); the next block is
+// requested as soon as they are there.  Blocks
 // past the last are requested past the end of the buffer, which reads zeros
-// and moves nothing.
-template <int MT, int RT, bool TILED, bool WIDE, int NW, int U>
+// and moves nothing.  ONCE: the matrix is read by this one pass and goes past
+// the caches.
+// A wave's LDS accesses before this come before those after it.
+__device__ __forceinline__ void lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int MT, int RT, bool TILED, bool WIDE, int NW, int U, bool ONCE>
 __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
-    __shared__ f32x4 red[NW][MT * RT][64];
+    constexpr int kTurn = 128 * ((TILED ? 0 : RT) + MT), kRed = 64 * MT * RT;
+    __shared__ u32x4 lds[NW][kTurn > kRed ? kTurn : kRed];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    u32x4* turn = lds[wave];
     const int r = lane & 15, g = lane >> 4;
     const int64_t tile0 = (int64_t)blockIdx.x * RT;
     const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
@@ -152,21 +171,20 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.codes + 16 * tile0 * p.K, w_bytes);
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.x + m0 * p.K, x_bytes);
     const float* sw = p.s_w + 16 * tile0 / kFp8Block * p.KB;
-    uint32_t wo[RT], xo[MT];
+    // Row-major: lanes 8 i .. 8 i + 7 read the 128 bytes of row i, then of row 8 + i.
+    uint32_t wo[RT], wo8[RT], xo[MT], xo8[MT];
     const float* sx[MT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < RT; ++t) {
         wo[t] = TILED ? (uint32_t)min(t, rw / 16 - 1) * 16u * (uint32_t)p.K + 16u * lane
-                      : (uint32_t)min(16 * t + (r & 7), rw - 1) * (uint32_t)p.K + 16u * g + 64u * (r >> 3);
-    uint32_t wo8[RT];  // row-major: rows 8 .. 15 of each 16
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-        wo8[t] = (uint32_t)min(16 * t + 8 + (r & 7), rw - 1) * (uint32_t)p.K + 16u * g + 64u * (r >> 3);
+                      : (uint32_t)min(16 * t + (lane >> 3), rw - 1) * (uint32_t)p.K + 16u * (lane & 7);
+        wo8[t] = (uint32_t)min(16 * t + 8 + (lane >> 3), rw - 1) * (uint32_t)p.K + 16u * (lane & 7);
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int m = min(16 * t + r, rx - 1);
-        xo[t] = (uint32_t)m * (uint32_t)p.K + 16u * g;
-        sx[t] = p.s_x + m0 + m;
+        xo[t] = (uint32_t)min(16 * t + (lane >> 3), rx - 1) * (uint32_t)p.K + 16u * (lane & 7);
+        xo8[t] = (uint32_t)min(16 * t + 8 + (lane >> 3), rx - 1) * (uint32_t)p.K + 16u * (lane & 7);
+        sx[t] = p.s_x + m0 + min(16 * t + r, rx - 1);
     }
 
     u32x4 wb[U][RT][2], xb[U][MT][2];
@@ -178,14 +196,14 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const uint32_t o = in ? wo[t] + ws : w_bytes;
-            wb[u][t][0] = load16(wr, o);
-            wb[u][t][1] = load16(wr, !in ? w_bytes : TILED ? o + 1024u : wo8[t] + ws);
+            const uint32_t o2 = !in ? w_bytes : TILED ? o + 1024u : wo8[t] + ws;
+            wb[u][t][0] = ONCE ? load16_nt(wr, o) : load16(wr, o);
+            wb[u][t][1] = ONCE ? load16_nt(wr, o2) : load16(wr, o2);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const uint32_t o = in ? xo[t] + xs : x_bytes;
-            xb[u][t][0] = load16(xr, o);
-            xb[u][t][1] = load16(xr, in ? o + 64u : x_bytes);
+            xb[u][t][0] = load16(xr, in ? xo[t] + xs : x_bytes);
+            xb[u][t][1] = load16(xr, in ? xo8[t] + xs : x_bytes);
             sb[u][t] = sx[t][(int64_t)kc * p.M];
         }
         swb[u] = sw[kc];
@@ -200,45 +218,67 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
     for (int kb = wave; kb < p.KB; kb += NW * U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // Row-major rows are loaded in whole lines, eight rows at a time: lane
-            // (r, g) holds bytes 16 g + 64 (r / 8) of rows r % 8 and 8 + r % 8.
-            // Lanes r and r ^ 8 exchange what belongs to the other's row.
-            if constexpr (!TILED) {
+            // Through LDS into the order of the matrix instruction; a wave's own part, so that
+            // it waits for no other.
+            auto put = [&](int t, const u32x4* v) __attribute__((always_inline)) {
 #pragma unroll
-                for (int b = 0; b < RT; ++b)
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 8 * h + (lane >> 3);
+                    turn[128 * t + 8 * row + swz<8>(row, lane & 7)] = v[h];
+                }
+            };
+            auto get = [&](int t, u32x4* v) __attribute__((always_inline)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t lo = wb[u][b][0][i], hi = wb[u][b][1][i];
-                        const uint32_t got = (uint32_t)dpp_mov<0x128>((int)(r < 8 ? hi : lo));  // row_ror:8
-                        wb[u][b][0][i] = r < 8 ? lo : got;
-                        wb[u][b][1][i] = r < 8 ? got : hi;
-                    }
+                for (int h = 0; h < 2; ++h) v[h] = turn[128 * t + 8 * r + swz<8>(r, g + 4 * h)];
+            };
+            u32x4 fw[RT][2], fx[MT][2];
+            float c[MT];
+#pragma unroll
+            for (int b = 0; b < RT; ++b) {
+                if constexpr (TILED) {
+                    fw[b][0] = wb[u][b][0];
+                    fw[b][1] = wb[u][b][1];
+                } else {
+                    put(MT + b, wb[u][b]);
+                }
             }
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
-                const Operand<WIDE> bx = operand<WIDE>(xb[u][a][0], xb[u][a][1]);
-                const float c = sb[u][a] * swb[u];
-#pragma unroll
-                for (int b = 0; b < RT; ++b) {
-                    const f32x4 d = block_product<WIDE>(operand<WIDE>(wb[u][b][0], wb[u][b][1]), bx);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][b][i] = __builtin_fmaf(d[i], c, acc[a][b][i]);
-                }
+                put(a, xb[u][a]);
+                c[a] = sb[u][a] * swb[u];
             }
             request(u, kb + NW * (U + u));
+            lds_order();
+            if constexpr (!TILED)
+#pragma unroll
+                for (int b = 0; b < RT; ++b) get(MT + b, fw[b]);
+#pragma unroll
+            for (int a = 0; a < MT; ++a) get(a, fx[a]);
+            lds_order();
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                const Operand<WIDE> bx = operand<WIDE>(fx[a][0], fx[a][1]);
+#pragma unroll
+                for (int b = 0; b < RT; ++b) {
+                    const f32x4 d = block_product<WIDE>(operand<WIDE>(fw[b][0], fw[b][1]), bx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[a][b][i] = __builtin_fmaf(d[i], c[a], acc[a][b][i]);
+                }
+            }
         }
     }
+    f32x4* red = reinterpret_cast<f32x4*>(turn);
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int b = 0; b < RT; ++b) red[wave][a * RT + b][lane] = acc[a][b];
+        for (int b = 0; b < RT; ++b) red[64 * (a * RT + b) + lane] = acc[a][b];
     __syncthreads();
     const Out o = output_of(p);
     for (int q = threadIdx.x; q < MT * RT * 64; q += 64 * NW) {
         const int t = q >> 6, l = q & 63;
-        f32x4 v = red[0][t][l];
+        f32x4 v = reinterpret_cast<const f32x4*>(lds[0])[64 * t + l];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) v += red[w][t][l];
+        for (int w = 1; w < NW; ++w) v += reinterpret_cast<const f32x4*>(lds[w])[64 * t + l];
         const int64_t m = m0 + 16 * (t / RT) + (l & 15);
         const int64_t n = 16 * (tile0 + t % RT) + 4 * (l >> 4);
         if (m < p.M && n < p.N) store4(o, m, n, v);
@@ -542,17 +582,18 @@ __global__ __launch_bounds__(kThreads) void fp8_join_kernel(Fp8Params p) {
     }
 }
 
-template <int MT, int RT, bool WIDE, int NW, int U>
+template <int MT, int RT, bool WIDE, int NW, int U, bool ONCE>
 hipError_t run_stream(const Fp8Params& p, bool t16, hipStream_t st) {
     const dim3 grid((uint32_t)((p.N + 16 * RT - 1) / (16 * RT)), (uint32_t)((p.M + 16 * MT - 1) / (16 * MT)));
-    if (t16) fp8_stream_kernel<MT, RT, true, WIDE, NW, U><<<grid, 64 * NW, 0, st>>>(p);
-    else fp8_stream_kernel<MT, RT, false, WIDE, NW, U><<<grid, 64 * NW, 0, st>>>(p);
+    if (t16) fp8_stream_kernel<MT, RT, true, WIDE, NW, U, ONCE><<<grid, 64 * NW, 0, st>>>(p);
+    else fp8_stream_kernel<MT, RT, false, WIDE, NW, U, ONCE><<<grid, 64 * NW, 0, st>>>(p);
     return hipGetLastError();
 }
 
 // cols: columns of tiles of kind A (all of them where that is enough).
 template <class A, class B, bool WIDE>
 hipError_t run_tiles(Fp8Params p, bool t16, hipStream_t st, int64_t cols, int parts) {
+    if (parts > p.KB) return hipErrorInvalidValue;  // a part without a block has no steps to read
     p.tiles_m = (int)((p.M + A::BM - 1) / A::BM);
     p.tiles_n = (int)((p.N + A::BN - 1) / A::BN);
     p.tiles_m2 = p.tiles_n2 = 0;
@@ -589,13 +630,13 @@ struct TileCost {
     int bm, bn;
     double start, step, more;
 };
-constexpr TileCost kNarrow[] = {{64, 64, 4.5, 0.31, 0.20}, {128, 128, 5, 0.53, 0.54}, {256, 128, 6, 0.90, 0.95},
-                                {256, 256, 8, 1.50, 1.60}};
+constexpr TileCost kNarrow[] = {{64, 64, 4.5, 0.31, 0.20}, {128, 128, 5, 0.58, 0.54}, {256, 128, 6, 0.90, 0.95},
+                                {256, 256, 8, 1.42, 1.60}};
 constexpr TileCost kWide[] = {{64, 64, 4.5, 0.47, 0.33}, {128, 128, 5, 0.98, 1.08}, {256, 128, 6, 1.70, 1.85}};
 
 struct Fp8Plan {
     bool stream;
-    int kind, parts;
+    int kind, parts;  // of a stream, 16-row tiles per workgroup
     int64_t cols;  // kXL: columns of tiles before kL takes over
     double us;
 };
@@ -607,19 +648,34 @@ double tiles_us(const TileCost& t, int64_t tiles, double blocks) {
     return blocks * (t.step + (double)(c - 1) * t.more);
 }
 
-// Streams read the matrix once per 32 tokens and both operands per workgroup's
-// outputs (16 or 32 matrix rows x 32 tokens): 4 us, then 6.5 TB/s of the one and
-// 16 TB/s of the other, or 66 bytes per ns of a CU where few have work (64 x 4096
-// x 4096 8.0 us, 64 x 11008 x 4096 21.3, 32 x 11008 x 4096 17).
-bool stream_narrow(int64_t m, int64_t n) { return ceil_div(n, 16) * ceil_div(m, 32) <= kCUs; }
+// A stream's workgroups of 16 `tiles` matrix rows: `own` us per k where each CU
+// has one, `more` + `more_k` k for each further round of them, besides the reading
+// of the matrix (fitted to 1000 sizes of up to 300 tokens, of which the three m <= 16 and
+// the two for more miss the time by 6 % and 8 % on average).
+struct StreamCost {
+    int tiles;
+    double own, more, more_k;
+};
+constexpr StreamCost kFew[] = {{1, 4.2e-4, 0.46, 3.6e-4}, {2, 6.4e-4, 0.49, 5.5e-4}, {4, 12.4e-4, 0.61, 11e-4}};
+constexpr StreamCost kMany[] = {{1, 6.6e-4, 1.2, 6.0e-4}, {2, 8.0e-4, 0.82, 8.3e-4}};
 
-double stream_us(int64_t m, int64_t n, int64_t k) {
-    const double nk = (double)n * (double)k;
-    if (m <= 16) return 4 + nk / 6.5e6;
-    const int rows = stream_narrow(m, n) ? 16 : 32;
-    const double per = (double)(rows + 32) * (double)k, wgs = (double)ceil_div(n, rows) * (double)ceil_div(m, 32);
-    const double all = nk / 6.5e6 + wgs * per / 16e6, one = (double)ceil_div((int64_t)wgs, kCUs) * per / 66e3;
-    return 4 + (all > one ? all : one);
+// Rows per workgroup by the expected time (in tiles, 16, 32 and 64 rows: 16 x 11008 x
+// 4096 11.2, 11.5, 10.2 us; 16 x 22016 x 4096 19.6, 16.5, 19.4; 64 x 4096 x 4096 10.0,
+// 6.5, -).
+double stream_us(int64_t m, int64_t n, int64_t k, int* tiles) {
+    const double read = (double)n * (double)k / (m <= 16 ? 14e6 : 10.4e6);
+    double best = 0.0;
+    *tiles = 0;
+    for (int i = 0; i < (m <= 16 ? 3 : 2); ++i) {
+        const StreamCost& c = m <= 16 ? kFew[i] : kMany[i];
+        const int64_t rounds = ceil_div(ceil_div(n, 16 * c.tiles) * ceil_div(m, m <= 16 ? 16 : 32), kCUs);
+        const double us = 3 + read + c.own * (double)k + (double)(rounds - 1) * (c.more + c.more_k * (double)k);
+        if (*tiles == 0 || us < best) {
+            best = us;
+            *tiles = c.tiles;
+        }
+    }
+    return best;
 }
 
 // Parts of k: their fp32 sums are written and read again, by a second launch
@@ -629,16 +685,20 @@ double join_us(int64_t m, int64_t n, int parts) {
 }
 
 Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int yt) {
-    Fp8Plan best = {true, 0, 1, 0, stream_us(m, n, k)};
+    Fp8Plan best = {true, 0, 1, 0, 0.0};
+    best.us = stream_us(m, n, k, &best.kind);
     if (m <= 16) return best;
+    if (m > kStreamTokens) best.us = 1e300;
     const int64_t kb = k / kFp8Block;
+    const double read = (double)n * (double)k / 5e6;  // the matrix from memory
     const TileCost* cost = yt == 0 ? kWide : kNarrow;
     for (int kind = kS; kind <= (yt == 0 ? kL : kXL); ++kind) {
         const TileCost& t = cost[kind];
         const int64_t tiles = ceil_div(m, t.bm) * ceil_div(n, t.bn);
         for (int parts = 1; parts <= kMaxParts && parts <= kb; ++parts) {
             if (parts > 1 && tiles * (parts - 1) >= 2 * kCUs) break;  // CUs enough without
-            const double us = t.start + tiles_us(t, tiles * parts, (double)ceil_div(kb, parts)) + join_us(m, n, parts);
+            if (tiles * parts >= kMaxGroups) break;
+            const double us = t.start + fmax(tiles_us(t, tiles * parts, (double)ceil_div(kb, parts)), read) + join_us(m, n, parts);
             if (us < best.us) best = {false, kind, parts, n, us};
         }
     }
@@ -691,15 +751,20 @@ hipError_t launch_qgemm_fp8(const Fp8GemmArgs& a, hipStream_t st) {
     p.sums = static_cast<float*>(a.ws);
     const Fp8Plan plan = plan_fp8(a.m, a.n, a.k, a.yt);
     if (!plan.stream) return a.yt == 0 ? run_plan<true>(p, a.t16, plan, st) : run_plan<false>(p, a.t16, plan, st);
-    // Streams: 32 matrix rows per workgroup where 16 give more than two to a CU
-    // (16 x 22016 x 4096: 23.6 -> 18.7 us in tiles; 16 x 4096 x 4096: 5.4 against 5.8)
-    const int64_t tiles = ceil_div(a.n, 16);
+    // Up to 32 tokens are one pass over the matrix: past the caches, which do not hold
+    // it then (1 x 4096 x 4096 5.7 -> 5.3 us, 16 x 22016 x 4096 19.0 -> 17.2).
     if (a.m <= 16) {
-        if (tiles <= 4 * kCUs) return run_stream<1, 1, true, 8, 2>(p, a.t16, st);
-        return run_stream<1, 2, true, 8, 1>(p, a.t16, st);
+        if (plan.kind == 4) return run_stream<1, 4, true, 8, 1, true>(p, a.t16, st);
+        if (plan.kind == 2) return run_stream<1, 2, true, 8, 1, true>(p, a.t16, st);
+        if (a.k > 4096) return run_stream<1, 1, true, 16, 1, true>(p, a.t16, st);  // 1 x 4096 x 11008 11.8 -> 11.2 us
+        return run_stream<1, 1, true, 8, 2, true>(p, a.t16, st);
     }
-    if (stream_narrow(a.m, a.n)) return run_stream<2, 1, true, 8, 2>(p, a.t16, st);
-    return run_stream<2, 2, true, 8, 1>(p, a.t16, st);
+    if (a.m <= 32) {
+        if (plan.kind == 2) return run_stream<2, 2, true, 8, 1, true>(p, a.t16, st);
+        return run_stream<2, 1, true, 8, 2, true>(p, a.t16, st);
+    }
+    if (plan.kind == 2) return run_stream<2, 2, true, 8, 1, false>(p, a.t16, st);
+    return run_stream<2, 1, true, 8, 2, false>(p, a.t16, st);
 }
 
 }  // namespace qg

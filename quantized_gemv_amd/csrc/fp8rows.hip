@@ -341,7 +341,7 @@ hipError_t pick_rows(const RowParams& p, hipStream_t st) {
     if (k8 <= 1024) return run_rows<OP, XT, RES, 512, 2>(p, st);
     if (k8 <= 1536 && p.rows > kFewRows) return run_rows<OP, XT, RES, 512, 3>(p, st);
     if (k8 <= 2048) return run_rows<OP, XT, RES, 1024, 2>(p, st);
-    if (k8 <= 3072) return run_rows<OP, XT, RES, 1024, 3>(p, st);
+    if (k8 <= 3 * 1024) return run_rows<OP, XT, RES, 1024, 3>(p, st);
     return run_rows<OP, XT, RES, 1024, 4>(p, st);  // up to 32768 values
 }
 

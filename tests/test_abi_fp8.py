@@ -134,7 +134,8 @@ def test_validation_product(qg):
         assert product(fmt=fmt) == ARG
     assert product(yt=2) == ARG and product(yt=-1) == ARG
     for bad in (dict(k=0), dict(k=64), dict(k=192), dict(k=qg.QG_BATCH_MAX_K + 128), dict(m=0), dict(m=1 << 30), dict(n=0),
-                dict(n=1 << 26), dict(m=1 << 29, k=4096), dict(n=1 << 25, k=65536), dict(m=1 << 20, n=1 << 19)):
+                dict(n=1 << 26), dict(m=1 << 29, k=4096), dict(n=1 << 25, k=65536), dict(m=1 << 20, n=1 << 19), dict(m=1 << 28, n=1),
+                dict(m=(1 << 20) + 1, n=1 << 16)):
         assert product(**bad) == SHAPE, bad
     for name in ("x", "y", "codes"):
         assert product(**{name: U}) == ALIGN

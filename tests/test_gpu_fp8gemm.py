@@ -77,7 +77,9 @@ SHAPES = [(1, 1, 128), (1, 16, 256), (1, 4096, 4096), (2, 130, 1152), (5, 257, 1
           (17, 130, 256), (31, 64, 1024), (32, 515, 640), (33, 128, 2176), (47, 2000, 384), (48, 36, 4096), (49, 16, 128),
           (61, 1411, 2048), (64, 256, 1024), (65, 130, 384), (100, 384, 512), (127, 250, 256), (128, 128, 128),
           (129, 129, 1408), (200, 1000, 2048), (255, 33, 640), (256, 256, 4096), (257, 258, 384), (300, 640, 1152),
-          (513, 511, 256), (700, 96, 2048), (1025, 300, 128)]
+          (513, 511, 256), (700, 96, 2048), (1025, 300, 128), (7, 100, 8320), (16, 4200, 256), (3, 9000, 128),
+          (12, 11000, 384), (18, 4200, 128), (29, 9010, 256), (32, 4097, 256), (40, 4200, 256), (64, 3000, 128),
+          (129, 129, 11008), (150, 203, 8192), (333, 1500, 1408), (600, 1300, 1152)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -98,7 +100,8 @@ def test_product(qg, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 300, 1024), (16, 48, 4096), (40, 130, 512), (64, 500, 256), (130, 260, 1152),
-                                   (300, 700, 640), (512, 512, 512)])
+                                   (300, 700, 640), (512, 512, 512), (600, 1300, 1152), (1300, 2100, 640),
+                                   (200, 300, 8192)])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
     """Every output told apart: whole codes, steps that are powers of two."""
@@ -107,7 +110,7 @@ def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
     x, w = fp8.encode(g.integers(-8, 9, (m, k))), fp8.encode(g.integers(-8, 9, (n, k)))
     s_x = 2.0 ** g.integers(-2, 3, (k // 128, m)).astype(np.float32)
     s_w = 2.0 ** g.integers(-2, 3, (-(-n // 128), k // 128)).astype(np.float32)
-    ref, size, _ = fp8.product(x, s_x, w, s_w)
+    ref, size, _ = fp8.product(x, s_x, w, s_w, cut=False)
     assert size.max() * 16 < 2 ** 24  # in units of 2^-4
     W = weights(qg, w, s_w, tiled)
     y = host(run(qg, W, e4(x), dev(s_x)))
@@ -118,7 +121,8 @@ def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
 # every kind of tile, in parts of k and not, and two kinds in one launch; ends
 # inside tiles in both directions
 LARGE = [(300, 4096, 11008), (2048, 512, 8192), (700, 4100, 1152), (1000, 1003, 8192), (4096, 4352, 128), (4100, 4611, 256),
-         (2048, 2050, 4096), (513, 11008, 640), (9000, 128, 384), (130, 20001, 256), (4096, 8192, 384)]
+         (2048, 2050, 4096), (513, 11008, 640), (9000, 128, 384), (130, 20001, 256), (4096, 8192, 384), (1029, 2050, 1152),
+         (2500, 2601, 384), (600, 1100, 4096), (1683, 11827, 640), (200000, 16, 128)]
 
 
 @pytest.mark.parametrize("m,n,k", LARGE)
@@ -176,7 +180,7 @@ def test_workspaces(qg):
     del junk
 
 
-@pytest.mark.parametrize("m", [1, 16, 61, 130, 300])
+@pytest.mark.parametrize("m", [1, 16, 61, 130, 300, 9000])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_all_codes(qg, m, tiled):
     """Every pair of finite codes meets at least once; one-hot rows pick them."""
@@ -191,14 +195,15 @@ def test_all_codes(qg, m, tiled):
     w[:, :] = fin[:, None]
     s_x = np.ones((2, m), np.float32)
     s_w = np.ones((2, 2), np.float32)
-    ref, _, _ = fp8.product(x, s_x, w, s_w)
+    ref, _, _ = fp8.product(x, s_x, w, s_w, cut=False)
     W = weights(qg, w, s_w, tiled)
     y = host(run(qg, W, e4(x), dev(s_x)))
     assert np.array_equal(y, ref.astype(np.float32))
     assert np.array_equal(host(run(qg, W, e4(x), dev(s_x), torch.bfloat16)), f32_to_bf16_rne(y))
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 200, 1024), (20, 200, 512), (130, 200, 1024), (300, 300, 384)])
+@pytest.mark.parametrize("m,n,k", [(1, 200, 1024), (20, 200, 512), (130, 200, 1024), (300, 300, 384),
+                                   (260, 260, 8192), (600, 1300, 1152)])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_nan_reaches_its_outputs_only(qg, m, n, k, tiled):
     note("nan m=%d n=%d tiled=%s" % (m, n, tiled))
@@ -228,7 +233,7 @@ def test_large_steps_and_small_ones(qg):
         x, s_x, w, s_w = operands(g, m, 130, 256)
         for a, b in ((1e20, 1e-20), (1e-30, 1e25), (1e-20, 1e-10)):
             sx, sw = (s_x * np.float32(a)).astype(np.float32), (s_w * np.float32(b)).astype(np.float32)
-            ref, size, _ = fp8.product(x, sx, w, sw)
+            ref, size, _ = fp8.product(x, sx, w, sw, cut=False)
             y = host(run(qg, weights(qg, w, sw, True), e4(x), dev(sx)))
             assert np.all(np.abs(y - ref) <= 265 * HALF * size)
 
@@ -325,7 +330,7 @@ def test_two_streams_and_graphs(qg):
         assert all(torch.equal(a.y, w) for a, w in zip(launches, want))
 
 
-@pytest.mark.parametrize("t", [1, 16, 70, 300])
+@pytest.mark.parametrize("t", [1, 16, 70, 300, 1500])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_feed_forward(qg, t, tiled):
     """norm, gate and up, SwiGLU, down, as a layer runs them: each step against
