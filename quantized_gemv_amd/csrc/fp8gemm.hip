@@ -402,24 +402,21 @@ __device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int6
     static_assert(MT % XR == 0, "a whole turn of the ring per block");
     u32x4 fw[NT][2], fx[XR][2];
     float sx[XR], sw = 0.0f;
+    // Rows 16 further have the same permutation, so a tile's address is one lane's
+    // offset and a constant in the instruction (an offset per tile: 28 more additions
+    // beside 32 matrix instructions, 4096 x 4096 x 16384 203 -> 212 us).
     const int xrow = wm * R + r, wrow = wn * (16 * NT) + r;
+    const int xl = xrow * kFp8Block + 16 * swz<8>(xrow, g), xh = xrow * kFp8Block + 16 * swz<8>(xrow, g + 4);
+    const int wl = BM * kFp8Block + (TILED ? wn * NT * 2048 + 16 * lane : wrow * kFp8Block + 16 * swz<8>(wrow, g));
+    const int wh = TILED ? wl + 1024 : BM * kFp8Block + wrow * kFp8Block + 16 * swz<8>(wrow, g + 4);
     auto read_x = [&](const uint8_t* base, const uint8_t* sc, int b) __attribute__((always_inline)) {
-        const int row = xrow + 16 * b;
-        fx[b % XR][0] = *reinterpret_cast<const u32x4*>(base + row * kFp8Block + 16 * swz<8>(row, g));
-        fx[b % XR][1] = *reinterpret_cast<const u32x4*>(base + row * kFp8Block + 16 * swz<8>(row, g + 4));
-        sx[b % XR] = *reinterpret_cast<const float*>(sc + 4 * row);
+        fx[b % XR][0] = *reinterpret_cast<const u32x4*>(base + xl + 2048 * b);
+        fx[b % XR][1] = *reinterpret_cast<const u32x4*>(base + xh + 2048 * b);
+        sx[b % XR] = *reinterpret_cast<const float*>(sc + 4 * xrow + 64 * b);
     };
     auto read_w = [&](const uint8_t* base, int a) __attribute__((always_inline)) {
-        const uint8_t* wbase = base + BM * kFp8Block;
-        if constexpr (TILED) {
-            const uint8_t* q = wbase + (wn * NT + a) * 2048 + 16 * lane;
-            fw[a][0] = *reinterpret_cast<const u32x4*>(q);
-            fw[a][1] = *reinterpret_cast<const u32x4*>(q + 1024);
-        } else {
-            const int row = wrow + 16 * a;
-            fw[a][0] = *reinterpret_cast<const u32x4*>(wbase + row * kFp8Block + 16 * swz<8>(row, g));
-            fw[a][1] = *reinterpret_cast<const u32x4*>(wbase + row * kFp8Block + 16 * swz<8>(row, g + 4));
-        }
+        fw[a][0] = *reinterpret_cast<const u32x4*>(base + wl + 2048 * a);
+        fw[a][1] = *reinterpret_cast<const u32x4*>(base + wh + 2048 * a);
     };
     auto read_sw = [&](const uint8_t* sc) {
         return reinterpret_cast<const float*>(sc)[BM + wn * (BN / WAVES_N) / kFp8Block];
@@ -623,7 +620,7 @@ typedef Fp8Tile<64, 64, 2, 2, 4> TileS;
 // sizes alone.  A tile costs `step` per block of k where its CU has one, `more`
 // for each further one that shares the CU or comes after it (measured with all
 // CUs at work: clocks are lower then), and `start` per launch.  Taken at
-// 4096 x 4096 x 16384 (bf16 y: XL 214 us, L 246, M 277, S 420), 128 x 4096 x 4096
+// 4096 x 4096 x 16384 (bf16 y: XL 203 us, L 246, M 262, S 420), 128 x 4096 x 4096
 // (43, 28, 21, 15) and the shapes named below.
 enum TileKind { kS, kM, kL, kXL };
 struct TileCost {
@@ -703,7 +700,7 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int yt) {
         }
     }
     // whole rounds of XL, the rest of the matrix in L (2048 x 11008 x 4096: XL
-    // 118 us, L 106, 32 columns of XL and 22 of L 99)
+    // 110 us, L 104, 32 columns of XL and 22 of L 101)
     if (yt != 0) {
         const int64_t tm = ceil_div(m, cost[kXL].bm), tn = ceil_div(n, cost[kXL].bn), rounds = tm * tn / kCUs;
         const int64_t cols = rounds * kCUs / tm;
