@@ -1261,6 +1261,9 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor = None, s: torch.Tensor = None
     columns (qg_quantize_fp8). Returns (q float8_e4m3fn, s [cols/128][rows])."""
     _dev(x, "x", (torch.float32, torch.bfloat16))
     rows, cols = _rows_cols(x, "x")
+    given = [t for t in (q, s) if t is not None]
+    if given and torch.is_grad_enabled() and any(t.requires_grad for t in given):
+        raise ValueError("outputs are written without a gradient: one requires a gradient")
     # torch.empty_like and sizes that are no tuple take half the host time
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn) if q is None else _shaped(q, "q", x.shape, torch.float8_e4m3fn, x)
     if s is None:
@@ -1268,6 +1271,8 @@ def quantize_fp8(x: torch.Tensor, q: torch.Tensor = None, s: torch.Tensor = None
     else:
         _shaped(s, "s", (cols // QG_FP8_BLOCK, rows), torch.float32, x)
     _call("qg_quantize_fp8", x, x.data_ptr(), _xt(x), rows, cols, q.data_ptr(), s.data_ptr())
+    if given:
+        torch._C._increment_version(given)
     return q, s
 
 
@@ -1291,6 +1296,8 @@ def _check_fp8_weight(w: QWeight):
     n = -(-w.n // 16) * 16 if w.fmt == QG_WFMT_FP8_T16 else w.n
     if w.codes.numel() != n * w.k or w.scale.numel() != -(-w.n // QG_FP8_BLOCK) * (w.k // QG_FP8_BLOCK):
         raise ValueError("codes or scale do not hold a matrix of [%d][%d]" % (w.n, w.k))
+    if w.scale.dim() > 1 and w.scale.shape != (-(-w.n // QG_FP8_BLOCK), w.k // QG_FP8_BLOCK):
+        raise ValueError("scale must be [n/128][k/128]")
 
 
 class QgemmFp8Launch(_Launch):

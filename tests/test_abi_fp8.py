@@ -237,6 +237,26 @@ def test_outputs_that_require_a_gradient_are_refused(qg, monkeypatch):
     qg.rms_norm(x, torch.ones(256), residual=h)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+    s = torch.zeros(2, 4, requires_grad=True)
+    with pytest.raises(ValueError, match="gradient"):
+        qg.quantize_fp8(x, s=s)
+    s = torch.zeros(2, 4)
+    loss = (torch.ones(2, 4, requires_grad=True) * s).sum()
+    qg.quantize_fp8(x, s=s)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_steps_of_weights_in_the_other_order_are_refused(qg, monkeypatch):
+    from quantized_gemv_amd import _binding as b
+    monkeypatch.setattr(b, "_dev", lambda t, *a: t)
+    monkeypatch.setattr(b, "_call", lambda *a: None)
+    e4 = torch.float8_e4m3fn
+    x, s_x = torch.zeros(1, 384).to(e4), torch.zeros(3, 1)
+    for scale in (torch.zeros(2, 3), torch.zeros(6)):
+        qg.qgemm_fp8(qg.QWeight(qg.QG_WFMT_FP8, 200, 384, torch.zeros(200, 384).to(e4), scale), x, s_x)
+    with pytest.raises(ValueError, match="scale"):
+        qg.qgemm_fp8(qg.QWeight(qg.QG_WFMT_FP8, 200, 384, torch.zeros(200, 384).to(e4), torch.zeros(3, 2)), x, s_x)
 
 
 def test_launches_keep_their_memory(qg, monkeypatch):
