@@ -317,6 +317,7 @@ struct Fp8Tile {
     static_assert(BM % (16 * kNW) == 0 && BN % (8 * kNW) == 0 && BM % 64 == 0 && kFp8Block % (BN / WAVES_N) == 0,
                   "whole loads per wave, one step of w per wave");
     static constexpr int kLds = STAGES * kCodes + (STAGES + 1) * kScales;
+    static constexpr int kPerSimd = 160 * 1024 / kLds * kNW / 4;  // waves that the LDS has room for
 };
 
 template <class C, bool TILED, bool WIDE>
@@ -511,6 +512,22 @@ __device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int6
                     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads,
                     __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);  // vector instructions
                 }
+            } else if (b == 0) {  // the matrix rows' conversions among the instructions (128x128, 64x64: 3-4% of the time)
+                __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+#pragma unroll
+                for (int i = 0; i < 4 * NT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+                    if (i % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                }
+            } else {
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+#pragma unroll
+                for (int i = 0; i < 4 * NT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+                    if (i % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -545,9 +562,11 @@ __device__ __forceinline__ void tile_at(int64_t t, int tiles_m, int tiles_n, int
     tn = u / h;
 }
 
-// Tiles of kind A, then those of kind B for the matrix rows from n1 on.
+// Tiles of kind A, then those of kind B for the matrix rows from n1 on.  Registers for
+// as many waves as the LDS has room for: for more, 64 x 64 with widened codes moves sums
+// to and from the accumulation registers (4096 x 4096 x 4096 190 -> 178 us).
 template <class A, class B, bool TILED, bool WIDE>
-__global__ __launch_bounds__(64 * A::kNW) void fp8_tile_kernel(Fp8Params p) {
+__global__ __launch_bounds__(64 * A::kNW) __attribute__((amdgpu_waves_per_eu(2, A::kPerSimd))) void fp8_tile_kernel(Fp8Params p) {
     static_assert(A::kNW == B::kNW, "one size of workgroup");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[A::kLds > B::kLds ? A::kLds : B::kLds];
     const int64_t first = (int64_t)p.tiles_m * p.tiles_n * p.parts;
