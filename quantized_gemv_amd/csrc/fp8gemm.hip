@@ -308,13 +308,22 @@ struct Fp8Tile {
     static constexpr int kNW = WAVES_M * WAVES_N;
     static constexpr int MT = BM / WAVES_M / 16, NT = BN / WAVES_N / 16;
     static constexpr int kCodes = (BM + BN) * kFp8Block;
-    static constexpr int kHalf = BM / 16 / kNW;      // 1 KB loads per wave: half of x's rows,
-    static constexpr int kW = BN / 8 / kNW;          // all of the matrix's,
+    // Tiles of 16 tokens of a wave in the first part: half of them, or fewer where
+    // that gives every wave as many loads.
+    static constexpr int head() {
+        int h = MT / 2;
+        while (h * 2 * WAVES_M % kNW != 0) --h;
+        return h;
+    }
+    static constexpr int H = head();
+    static constexpr int kX1 = 2 * H * WAVES_M / kNW;         // 1 KB loads per wave: the first part's rows of x,
+    static constexpr int kX2 = 2 * (MT - H) * WAVES_M / kNW;  // the second's,
+    static constexpr int kW = BN / 8 / kNW;                   // all of the matrix's,
     static constexpr int kScaleLoads = BM / 64 + 1;  // and of all waves 64 steps of x each, then those of w
     static constexpr int kSL = (kScaleLoads + kNW - 1) / kNW;
     static constexpr int kScales = 256 * kScaleLoads;
-    static constexpr int kFirst = kW + kHalf + kSL, kSecond = kHalf;  // loads of a block's two parts
-    static_assert(BM % (16 * kNW) == 0 && BN % (8 * kNW) == 0 && BM % 64 == 0 && kFp8Block % (BN / WAVES_N) == 0,
+    static constexpr int kFirst = kW + kX1 + kSL, kSecond = kX2;  // loads of a block's two parts
+    static_assert(H > 0 && 2 * (MT - H) * WAVES_M % kNW == 0 && BN % (8 * kNW) == 0 && BM % 64 == 0 && kFp8Block % (BN / WAVES_N) == 0,
                   "whole loads per wave, one step of w per wave");
     static constexpr int kLds = STAGES * kCodes + (STAGES + 1) * kScales;
     static constexpr int kPerSimd = 160 * 1024 / kLds * kNW / 4;  // waves that the LDS has room for
@@ -333,18 +342,18 @@ __device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int6
     const int rx = (int)min((int64_t)BM, p.M - m0);
     const int64_t rows_w = TILED ? (p.N + 15) / 16 * 16 : p.N;
     const int rw = (int)min((int64_t)BN, rows_w - n0);
-    // This lane's 16 bytes at block 0 of each load: x's rows in halves (every
-    // wave row's first tokens, then its last), w's rows or tiles.
-    constexpr int R = BM / WAVES_M;  // tokens of a wave
-    auto x_row = [&](int half, int l) {
-        const int j = wave + NW * l;
-        return j / (R / 16) * R + half * (R / 2) + 8 * (j % (R / 16));
+    // This lane's 16 bytes at block 0 of each load: x's rows in two parts (every
+    // wave row's first tokens, then the rest), w's rows or tiles.
+    constexpr int R = BM / WAVES_M, H = C::H;  // tokens of a wave
+    auto x_row = [&](int part, int l) {
+        const int j = wave + NW * l, per = 2 * (part == 0 ? H : MT - H);
+        return j / per * R + (part == 0 ? 0 : 16 * H) + 8 * (j % per);
     };
-    uint32_t xo[2][C::kHalf], wo[C::kW];
+    uint32_t xo[2][C::kX1 > C::kX2 ? C::kX1 : C::kX2], wo[C::kW];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int l = 0; l < C::kHalf; ++l) {
+        for (int l = 0; l < (h == 0 ? C::kX1 : C::kX2); ++l) {
             const int row = x_row(h, l) + (lane >> 3);
             xo[h][l] = (uint32_t)min(row, rx - 1) * (uint32_t)p.K + 16u * swz<8>(row, lane & 7);
         }
@@ -383,10 +392,10 @@ __device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int6
             const __amdgpu_buffer_rsrc_t wr = make_rsrc(p.codes + n0 * p.K, kb < kb1 ? w_bytes : 0u);
             dma16_buffer(wr, smem + to * C::kCodes + (BM / 8 + wave + NW * i) * 1024, wo[i],
                          (uint32_t)kb * (TILED ? 2048u : 128u));
-        } else if (i < C::kW + C::kHalf) {
+        } else if (i < C::kW + C::kX1) {
             issue_x(0, i - C::kW, kb, to);
         } else {
-            const int l = i - C::kW - C::kHalf;
+            const int l = i - C::kW - C::kX1;
             dma4(ssrc[l] + (int64_t)min(kb, kb1 - 1) * sstr[l], smem + sdst[l] + sto * C::kScales);
         }
     };
@@ -399,8 +408,8 @@ __device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int6
 
     // Fragments and steps of a block, read from its LDS buffer.
     constexpr int LA = MT > 2 ? 2 : 1;
-    constexpr int XR = MT > 2 ? 4 : 2;
-    static_assert(MT % XR == 0, "a whole turn of the ring per block");
+    constexpr int XR = MT % 4 == 0 ? 4 : MT % 3 == 0 ? 3 : 2;
+    static_assert(MT % XR == 0 && XR > LA && H >= LA, "a whole turn of the ring per block");
     u32x4 fw[NT][2], fx[XR][2];
     float sx[XR], sw = 0.0f;
     // Rows 16 further have the same permutation, so a tile's address is one lane's
@@ -452,7 +461,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8Params& p, uint8_t* smem, int6
     for (int a = 0; a < NT; ++a) read_w(smem, a);
     sw = read_sw(scales);
 
-    constexpr int S1 = MT / 2 > LA ? MT / 2 - LA : 0, S2 = MT - LA;
+    constexpr int S1 = H - LA, S2 = MT - LA;
     int slot = 0, sslot = 0;  // of block kb; the steps have one buffer more, as they are read to the block's end
     for (int kb = kb0; kb < kb1; ++kb) {
         const uint8_t* here = smem + slot * C::kCodes;
@@ -632,6 +641,7 @@ hipError_t run_tiles(Fp8Params p, bool t16, hipStream_t st, int64_t cols, int pa
 
 typedef Fp8Tile<256, 256, 2, 4, 2> TileXL;
 typedef Fp8Tile<256, 128, 4, 2, 2> TileL;
+typedef Fp8Tile<192, 128, 2, 4, 2> TileH;
 typedef Fp8Tile<128, 128, 2, 4, 2> TileM;
 typedef Fp8Tile<64, 64, 2, 2, 4> TileS;
 
@@ -639,21 +649,24 @@ typedef Fp8Tile<64, 64, 2, 2, 4> TileS;
 // sizes alone.  A tile costs `step` per block of k where its CU has one, `more`
 // for each further one that shares the CU or comes after it (measured with all
 // CUs at work: clocks are lower then), and `start` per launch.  Taken at
-// 4096 x 4096 x 16384 (bf16 y: XL 203 us, L 246, M 262, S 420), 128 x 4096 x 4096
-// (43, 28, 21, 15) and the shapes named below.
-enum TileKind { kS, kM, kL, kXL };
+// 4096 x 4096 x 16384 (bf16 y: XL 203 us, L 244, H 293, M 262, S 420), 128 x 4096 x 4096
+// (XL 43, L 28, M 21, S 15), 1100 x 4096 x 4096 (L 32, H 27, M 34, S 45) and the shapes
+// named below.
+enum TileKind { kS, kM, kH, kL, kXL };
 struct TileCost {
     int bm, bn;
     double start, step, more;
 };
-constexpr TileCost kNarrow[] = {{64, 64, 4.5, 0.31, 0.20}, {128, 128, 5, 0.58, 0.54}, {256, 128, 6, 0.90, 0.95},
-                                {256, 256, 8, 1.42, 1.60}};
-constexpr TileCost kWide[] = {{64, 64, 4.5, 0.47, 0.33}, {128, 128, 5, 0.98, 1.08}, {256, 128, 6, 1.70, 1.85}};
+constexpr TileCost kNarrow[] = {{64, 64, 4.5, 0.31, 0.20}, {128, 128, 5, 0.58, 0.54}, {192, 128, 6, 0.74, 0.80},
+                                {256, 128, 6, 0.90, 0.95}, {256, 256, 8, 1.42, 1.60}};
+constexpr TileCost kWide[] = {{64, 64, 4.5, 0.47, 0.33}, {128, 128, 5, 0.98, 1.08}, {192, 128, 6, 1.28, 1.50},
+                              {256, 128, 6, 1.70, 1.85}};
 
 struct Fp8Plan {
     bool stream;
     int kind, parts;  // of a stream, 16-row tiles per workgroup
-    int64_t cols;  // kXL: columns of tiles before kL takes over
+    int64_t cols;  // kXL: columns of tiles before `rest` takes over
+    int rest;
     double us;
 };
 
@@ -695,13 +708,13 @@ double stream_us(int64_t m, int64_t n, int64_t k, int* tiles) {
 }
 
 // Parts of k: their fp32 sums are written and read again, by a second launch
-// (300 x 4096 x 11008: M whole 52.7 us, in 2 parts 35.8, in 5 34.3; L in 4 34.7).
+// (300 x 4096 x 11008: H whole 58.6 us, in 2 parts 39.1, in 4 31.5; L in 4 35.6).
 double join_us(int64_t m, int64_t n, int parts) {
     return parts == 1 ? 0.0 : 3.5 + 4.0 * parts * (double)m * (double)n / 3.5e6;
 }
 
 Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int yt) {
-    Fp8Plan best = {true, 0, 1, 0, 0.0};
+    Fp8Plan best = {true, 0, 1, 0, kL, 0.0};
     best.us = stream_us(m, n, k, &best.kind);
     if (m <= 16) return best;
     if (m > kStreamTokens) best.us = 1e300;
@@ -715,19 +728,19 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int yt) {
             if (parts > 1 && tiles * (parts - 1) >= 2 * kCUs) break;  // CUs enough without
             if (tiles * parts >= kMaxGroups) break;
             const double us = t.start + fmax(tiles_us(t, tiles * parts, (double)ceil_div(kb, parts)), read) + join_us(m, n, parts);
-            if (us < best.us) best = {false, kind, parts, n, us};
+            if (us < best.us) best = {false, kind, parts, n, kL, us};
         }
     }
-    // whole rounds of XL, the rest of the matrix in L (2048 x 11008 x 4096: XL
-    // 110 us, L 104, 32 columns of XL and 22 of L 101)
+    // whole rounds of XL, the rest of the matrix in L or H (2048 x 11008 x 4096: XL
+    // 111 us, L 109, 32 columns of XL and 22 of L 96, of H 92)
     if (yt != 0) {
         const int64_t tm = ceil_div(m, cost[kXL].bm), tn = ceil_div(n, cost[kXL].bn), rounds = tm * tn / kCUs;
         const int64_t cols = rounds * kCUs / tm;
-        if (rounds >= 1 && cols < tn) {
-            const int64_t rest = ceil_div(m, cost[kL].bm) * ceil_div(n - cols * cost[kXL].bn, cost[kL].bn);
+        for (int kind = kH; kind <= kL && rounds >= 1 && cols < tn; ++kind) {
+            const int64_t rest = ceil_div(m, cost[kind].bm) * ceil_div(n - cols * cost[kXL].bn, cost[kind].bn);
             const double us = cost[kXL].start + tiles_us(cost[kXL], tm * cols, (double)kb) +
-                              (double)kb * (double)ceil_div(rest, kCUs) * cost[kL].more;
-            if (us < best.us) best = {false, kXL, 1, cols, us};
+                              (double)kb * (double)ceil_div(rest, kCUs) * cost[kind].more;
+            if (us < best.us) best = {false, kXL, 1, cols, kind, us};
         }
     }
     return best;
@@ -738,10 +751,12 @@ hipError_t run_plan(const Fp8Params& p, bool t16, const Fp8Plan& plan, hipStream
     switch (plan.kind) {
         case kS: return run_tiles<TileS, TileS, WIDE>(p, t16, st, p.N, plan.parts);
         case kM: return run_tiles<TileM, TileM, WIDE>(p, t16, st, p.N, plan.parts);
+        case kH: return run_tiles<TileH, TileH, WIDE>(p, t16, st, p.N, plan.parts);
         case kL: return run_tiles<TileL, TileL, WIDE>(p, t16, st, p.N, plan.parts);
         default: break;
     }
     if constexpr (WIDE) return hipErrorInvalidValue;  // no plan of fp32 outputs has it
+    else if (plan.rest == kH) return run_tiles<TileXL, TileH, false>(p, t16, st, plan.cols, plan.parts);
     else return run_tiles<TileXL, TileL, false>(p, t16, st, plan.cols, plan.parts);
 }
 

@@ -100,7 +100,7 @@ def test_product(qg, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 300, 1024), (16, 48, 4096), (40, 130, 512), (64, 500, 256), (130, 260, 1152),
-                                   (300, 700, 640), (512, 512, 512), (600, 1300, 1152), (1300, 2100, 640),
+                                   (300, 700, 640), (512, 512, 512), (600, 1300, 1152), (1300, 2100, 640), (332, 13999, 256),
                                    (200, 300, 8192)])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
@@ -122,7 +122,8 @@ def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
 # inside tiles in both directions
 LARGE = [(300, 4096, 11008), (2048, 512, 8192), (700, 4100, 1152), (1000, 1003, 8192), (4096, 4352, 128), (4100, 4611, 256),
          (2048, 2050, 4096), (513, 11008, 640), (9000, 128, 384), (130, 20001, 256), (4096, 8192, 384), (1029, 2050, 1152),
-         (2500, 2601, 384), (600, 1100, 4096), (1683, 11827, 640), (200000, 16, 128)]
+         (2500, 2601, 384), (600, 1100, 4096), (1683, 11827, 640), (200000, 16, 128),
+         (785, 23363, 640), (387, 11809, 640), (197, 8343, 4864), (969, 1318, 4480), (450, 10265, 384), (162, 5545, 3712)]
 
 
 @pytest.mark.parametrize("m,n,k", LARGE)
@@ -203,7 +204,7 @@ def test_all_codes(qg, m, tiled):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 200, 1024), (20, 200, 512), (130, 200, 1024), (300, 300, 384),
-                                   (260, 260, 8192), (600, 1300, 1152)])
+                                   (260, 260, 8192), (600, 1300, 1152), (136, 5641, 3456)])
 @pytest.mark.parametrize("tiled", [False, True])
 def test_nan_reaches_its_outputs_only(qg, m, n, k, tiled):
     note("nan m=%d n=%d tiled=%s" % (m, n, tiled))
