@@ -1281,8 +1281,8 @@ def quantize_fp8_weight(w: torch.Tensor) -> QWeight:
     (qg_quantize_fp8_weight), as QG_WFMT_FP8. tiled16 lays them out in tiles."""
     _dev(w, "w", (torch.float32, torch.bfloat16))
     n, k = _rows_cols(w, "w")
-    codes = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=w.device)
-    scale = torch.empty((-(-n // QG_FP8_BLOCK), k // QG_FP8_BLOCK), dtype=torch.float32, device=w.device)
+    codes = torch.empty_like(w, dtype=torch.float8_e4m3fn)
+    scale = torch.empty(-(-n // QG_FP8_BLOCK), k // QG_FP8_BLOCK, dtype=torch.float32, device=w.device)
     _call("qg_quantize_fp8_weight", w, w.data_ptr(), _xt(w), n, k, codes.data_ptr(), scale.data_ptr())
     return QWeight(QG_WFMT_FP8, n, k, codes, scale)
 

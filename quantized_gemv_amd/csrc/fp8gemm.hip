@@ -295,10 +295,10 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
 // What bounds it is the loads into LDS (from the L2s about 65 bytes per ns and
 // CU with all of them at work), so they never stop: a buffer is refilled in two
 // parts while its block is still multiplied.  The matrix rows' fragments and
-// those of the first half of a wave's tokens are in registers first (a
-// group of 16 tokens is read LA groups ahead); once every wave has them, that
-// part is requested again (S1), the second half when that is read (S2), each
-// 1.5 blocks before it is wanted.  The loads are spread between the matrix
+// those of the first part of a wave's tokens (half or fewer) are in registers
+// first (a group of 16 tokens is read LA groups ahead); once every wave has them,
+// that part is requested again (S1), the second part when that is read (S2), each
+// about 1.5 blocks before it is wanted.  The loads are spread between the matrix
 // instructions (at once, a wave would stand still until the address unit has
 // taken all of them: 2.45 -> 2.57 PFLOP/s at 4096 x 4096 x 16384), and the
 // products of kLag instructions ago take their steps beside them.
