@@ -89,7 +89,9 @@ __device__ __forceinline__ u32x4 bf16_pack8(const float v[8]) {
     for (int j = 0; j < 4; ++j) o[j] = any_f32_to_bf16(v[2 * j]) | (any_f32_to_bf16(v[2 * j + 1]) << 16);
     return o;
 }
-// Eight values at element e of a float output (0: fp32, 1: bf16).
+// Eight values at element e of a float output (0: fp32, 1: bf16).  PAST: past
+// the caches.
+template <bool PAST = false>
 __device__ __forceinline__ void store8(void* y, int yt, int64_t e, const float v[8]) {
     if (yt == 0) {
         u32x4* p = reinterpret_cast<u32x4*>(static_cast<float*>(y) + e);
@@ -99,10 +101,17 @@ __device__ __forceinline__ void store8(void* y, int yt, int64_t e, const float v
             a[j] = __float_as_uint(v[j]);
             b[j] = __float_as_uint(v[4 + j]);
         }
-        p[0] = a;
-        p[1] = b;
+        if constexpr (PAST) {
+            __builtin_nontemporal_store(a, p);
+            __builtin_nontemporal_store(b, p + 1);
+        } else {
+            p[0] = a;
+            p[1] = b;
+        }
     } else {
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(y) + e) = bf16_pack8(v);
+        u32x4* p = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(y) + e);
+        if constexpr (PAST) __builtin_nontemporal_store(bf16_pack8(v), p);
+        else *p = bf16_pack8(v);
     }
 }
 
