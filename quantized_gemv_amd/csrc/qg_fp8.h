@@ -52,21 +52,17 @@ __device__ __forceinline__ uint2 fp8_codes8(const float v[8], float i) {
 }
 
 // Eight consecutive values as they stand in memory: one 16-byte load of bf16,
-// two of fp32.
+// two of fp32.  PAST: past the caches.
 template <int XT>
 struct Raw8 {
     u32x4 w[XT == 0 ? 2 : 1];
 };
-template <int XT>
+template <int XT, bool PAST = false>
 __device__ __forceinline__ Raw8<XT> raw8(const void* base, int64_t e) {
     Raw8<XT> r;
-    if constexpr (XT == 0) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + e);
-        r.w[0] = p[0];
-        r.w[1] = p[1];
-    } else {
-        r.w[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + e);
-    }
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) + e * (XT == 0 ? 4 : 2));
+    r.w[0] = PAST ? __builtin_nontemporal_load(p) : p[0];
+    if constexpr (XT == 0) r.w[1] = PAST ? __builtin_nontemporal_load(p + 1) : p[1];
     return r;
 }
 template <int XT>
