@@ -736,7 +736,7 @@ Fp8Plan plan_fp8(int64_t m, int64_t n, int64_t k, int yt) {
     if (yt != 0) {
         const int64_t tm = ceil_div(m, cost[kXL].bm), tn = ceil_div(n, cost[kXL].bn), rounds = tm * tn / kCUs;
         const int64_t cols = rounds * kCUs / tm;
-        for (int kind = kH; kind <= kL && rounds >= 1 && cols < tn; ++kind) {
+        for (int kind = kH; kind <= kL && cols >= 1 && cols < tn; ++kind) {
             const int64_t rest = ceil_div(m, cost[kind].bm) * ceil_div(n - cols * cost[kXL].bn, cost[kind].bn);
             const double us = cost[kXL].start + tiles_us(cost[kXL], tm * cols, (double)kb) +
                               (double)kb * (double)ceil_div(rest, kCUs) * cost[kind].more;

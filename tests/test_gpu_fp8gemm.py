@@ -123,7 +123,8 @@ def test_exact_where_sums_are_whole(qg, m, n, k, tiled):
 LARGE = [(300, 4096, 11008), (2048, 512, 8192), (700, 4100, 1152), (1000, 1003, 8192), (4096, 4352, 128), (4100, 4611, 256),
          (2048, 2050, 4096), (513, 11008, 640), (9000, 128, 384), (130, 20001, 256), (4096, 8192, 384), (1029, 2050, 1152),
          (2500, 2601, 384), (600, 1100, 4096), (1683, 11827, 640), (200000, 16, 128),
-         (785, 23363, 640), (387, 11809, 640), (197, 8343, 4864), (969, 1318, 4480), (450, 10265, 384), (162, 5545, 3712)]
+         (785, 23363, 640), (387, 11809, 640), (197, 8343, 4864), (969, 1318, 4480), (450, 10265, 384), (162, 5545, 3712),
+         (70000, 250, 256), (1100000, 16, 128)]
 
 
 @pytest.mark.parametrize("m,n,k", LARGE)
