@@ -143,10 +143,10 @@ __device__ __forceinline__ Out output_of(const Fp8Params& p) { return {p.y, p.yt
 // through the wave's own LDS into the order of the matrix instruction (requested
 // in that order, 16 bytes here and there: 16 x 22016 x 4096 row-major 22.5 against
 // 19.0 us, 64 x 11008 x 4096 in tiles 21.5 against 17.4); the next block is
-// requested as soon as they are there.  Blocks
-// past the last are requested past the end of the buffer, which reads zeros
-// and moves nothing.  ONCE: the matrix is read by this one pass and goes past
-// the caches.
+// requested as soon as they are there.  Blocks past the last are requested past
+// the end of the buffer, which reads zeros and moves nothing; their step is 0, as
+// the last block's, which is read again for them, may be infinite.  ONCE: the
+// matrix is read by this one pass and goes past the caches.
 // A wave's LDS accesses before this come before those after it.
 __device__ __forceinline__ void lds_order() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -245,7 +245,8 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Params p) {
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
                 put(a, xb[u][a]);
-                c[a] = sb[u][a] * swb[u];
+                const float step = sb[u][a] * swb[u];
+                c[a] = u == 0 || kb + NW * u < p.KB ? step : 0.0f;
             }
             request(u, kb + NW * (U + u));
             lds_order();
