@@ -27,13 +27,24 @@ enum { kOpNone = 0, kOpNorm = 1, kOpSwiglu = 2 };
 // Over an input, whose lines are there already, 10.8 -> 11.4).
 enum { kNone = 0, kInPlace = 1, kPast = 2 };
 
-// The quotient by v_rcp_f32 (1 ulp) and the exponential by v_exp_f32 (its
-// argument rounded to fp32: the result is off by up to |g| 2^-24 of itself):
-// correctly rounded ones would take more time than the memory, at 8 bytes or
-// fewer per value.
-__device__ __forceinline__ float swiglu_fast(float g, float u) {
-    const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
-    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+// g / (1 + exp(-g)) * u.  With t = -g log2(e) / 2 rounded, exp(-g) is 4^t (1 + d), where d =
+// -g - 2 t ln 2 is what the rounding lost, and 2^t stays within fp32 for every gate that
+// matters; 1 + exp(-g), scaled by 2^-32, has its reciprocal (0 from exp(-g) = 2^158 on).  With
+// the hardware's 2^t and reciprocal (1 ulp each) the result is off by at most 10 half steps
+// and, from ln 2, |g| / 21 more, besides the 2^-149 steps of 1 / (1 + exp(-g)).  d, the scale and
+// the clamp (for infinite gates: -inf times 0 is NaN, as the quotient is) are 5 of 17 issue
+// slots: 2048 x 11008 bf16 to e4m3 22.1 -> 24.1 us back to back, a feed-forward with its
+// products the same within 1%.  Without them the error is 1.2 |g| half steps and gates
+// below -87.3 give 0; 2^n and 2^rest apart, for 8.4 half steps in 23 slots, took 26.4 us.
+__device__ __forceinline__ float swiglu_of(float g, float u) {
+    constexpr float kScale = 2.32830644e-10f;  // 2^-32
+    const float c = __builtin_amdgcn_fmed3f(g, -170.0f, 170.0f);
+    const float t = c * -0.721347511f;
+    const float d = __builtin_fmaf(t, -1.38629436f, -c);
+    const float p = __builtin_amdgcn_exp2f(t);
+    const float ps = p * kScale;
+    const float den = __builtin_fmaf(__builtin_fmaf(ps, d, ps), p, kScale);
+    return g * (__builtin_amdgcn_rcpf(den) * kScale) * u;
 }
 
 struct RowParams {
@@ -140,7 +151,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void fp8_row_kernel(RowParams p)
                     float b[8];
                     values8<XT>(rr[j], b);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = OP == kOpSwiglu ? swiglu_fast(v[j][i], b[i]) : v[j][i] + b[i];
+                    for (int i = 0; i < 8; ++i) v[j][i] = OP == kOpSwiglu ? swiglu_of(v[j][i], b[i]) : v[j][i] + b[i];
                     if constexpr (RES != kNone) {
                         if (live && in[j]) store8<RES == kPast>(p.residual_out, XT, row * p.k + at[j], v[j]);
                     }
@@ -247,9 +258,10 @@ __global__ __launch_bounds__(kThreads) void fp8_flat_kernel(RowParams p, int64_t
             row[j] = small ? (int64_t)((uint32_t)c[j] / (uint32_t)k8) : c[j] / k8;
             col[j] = c[j] - row[j] * k8;
             const int64_t e = 8 * (OP == kOpSwiglu ? 2 * row[j] * k8 + col[j] : c[j]);
-            // SwiGLU's x, a product's output, is wanted no more: past the caches (2048 x 11008
-            // bf16 to e4m3 22.9 -> 22.0 us, to bf16 26.8 -> 22.7; 1000 x 11008, which fits in
-            // them, 11.4 -> 12.2; a feed-forward with its products 1-2% less).
+            // SwiGLU's x, a product's output, is wanted no more: past the caches (4129 x 11008
+            // bf16 to e4m3 45.7 -> 43.5 us, 2048 x 11008 to bf16 27.5 -> 23.7, to e4m3 24.0 either
+            // way; 1000 x 11008, which fits in them, 12.2 -> 13.4; a feed-forward with its
+            // products up to 1% less).
             ra[j] = raw8<XT, OP == kOpSwiglu>(p.x, e);
             if constexpr (OP == kOpSwiglu) rb[j] = raw8<XT, true>(p.x, e + p.k);
         }
@@ -261,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void fp8_flat_kernel(RowParams p, int64_t
                 float b[8];
                 values8<XT>(rb[j], b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = swiglu_fast(v[i], b[i]);
+                for (int i = 0; i < 8; ++i) v[i] = swiglu_of(v[i], b[i]);
             }
             const bool live = c0 + j * kThreads < chunks;
             if (p.out <= 1) {

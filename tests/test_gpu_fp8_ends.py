@@ -5,11 +5,13 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import synth
-from gpu_util import dev
+from gpu_util import dev, dev_bf16, f32_to_bf16_rne, host
 from oracle import fp8
 
 pytestmark = pytest.mark.gpu
+HALF = 2.0 ** -24
 E4 = torch.float8_e4m3fn
 
 
@@ -78,3 +80,67 @@ def test_steps_without_an_end(qg, m, n, k, tiled):
         sx = s_x.copy()
         sx[-1, i] = np.inf
         assert np.all(np.isnan(y(sx, s_w, dtype, zero)[i]))
+
+
+def gates():
+    """Gates over the whole range, densely where exp(-|g|) is a number."""
+    near = np.concatenate([np.linspace(-110, 110, 40001), np.linspace(-88.9, -87.2, 4001),
+                           2.0 ** np.linspace(-140, 6, 2001), -2.0 ** np.linspace(-140, 6, 2001)])
+    far = np.array([0.0, -0.0, 1e4, -1e4, 1e10, -1e10, 1e30, 3e38, -1e30, -3e38, 126.5, -126.5, -149.0, -360.0, -362.0])
+    g = np.concatenate([near, far]).astype(np.float32)
+    return np.concatenate([g, np.zeros(-len(g) % 128, np.float32)])
+
+
+@pytest.mark.parametrize("up", [1.0, -1.7, 3e30, 1e-30, 2.0 ** -120])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_swiglu_over_the_range_of_fp32(qg, up, bf16):
+    """fp32 outputs.  In half steps: exp(-g) from the square of the hardware's 2^t
+    (one unit, 2, twice), the product that corrects it (1) and ln 2, whose fp32 value
+    is off by 2^-28.4 (|g| 2^-28.4, |g| / 21 half steps), all of it times 1 / (1 + exp(g)) <= 1; the
+    sum 1, the reciprocal 2 (one unit), two products 2: 10 + |g| / 21.  What is
+    below 2^-126 keeps steps of 2^-149, half of one each: 1 / (1 + exp(-g)), which goes times |g u|
+    (and where the scaled sum is above 2^126 its reciprocal, 2^-158, is 0), silu, which
+    goes times |u|, and the result."""
+    note("swiglu range up=%g bf16=%s" % (up, bf16))
+    g = gates()
+    n = len(g)
+    u = (up * (1 + np.arange(n) % 7 / 8)).astype(np.float32)
+    x = np.stack([np.concatenate([g, u]), np.concatenate([g, -u])])
+    if bf16:
+        bits = synth.to_bf16_bits(x)
+        x, xd = synth.bf16_bits_to_f32(bits), dev_bf16(bits)
+    else:
+        xd = dev(x)
+    gate, upv = x[:, :n].astype(np.float64), np.abs(x[:, n:].astype(np.float64))
+    ref = fp8.swiglu(x)
+    top = float(np.finfo(np.float32).max)
+    y = host(qg.swiglu(xd, out_dtype=torch.float32))
+    fits = np.abs(ref) <= top * (1 - 15 * HALF)  # gates from -88 on are below 15 half steps
+    gu = np.abs(gate) * upv
+    off = (10 + np.abs(gate) / 21) * HALF * np.abs(ref) + 2.0 ** -150 * ((1 + 2.0 ** -8) * gu + upv + 1)
+    err = np.abs(y.astype(np.float64) - ref)
+    worst = np.max(np.where(fits & (np.abs(ref) >= 2.0 ** -126) & (gate > -85) & (np.abs(gate) >= 2.0 ** -125), err / (HALF * np.maximum(np.abs(ref), 2.0 ** -126)), 0.0))
+    print("half steps, at worst: %.2f" % worst, flush=True)
+    assert np.all(err[fits] <= off[fits])
+    over = np.abs(ref) > top * (1 + 15 * HALF)
+    assert np.array_equal(y[over], np.copysign(np.inf, ref[over]).astype(np.float32))
+    # the other outputs are the roundings of the same values
+    assert np.array_equal(host(qg.swiglu(xd)), f32_to_bf16_rne(y))
+    for dtype, most in ((E4, 40064), (torch.int8, 32768)):  # gates of -110 .. 110 and of -110 .. 70
+        part = xd[:, torch.cat([torch.arange(most), n + torch.arange(most)]).cuda()].contiguous()
+        q, s = qg.swiglu(part, out_dtype=dtype)
+        if dtype == E4:
+            ref_q, ref_s = fp8.quantize(y[:, :most])
+            assert np.array_equal(host(s), ref_s) and np.array_equal(host(q.view(torch.uint8)), ref_q)
+        else:
+            ref_q, ref_s = oracle.quantize_absmax(y[:, :most], per_row=True)
+            assert np.array_equal(host(s), ref_s) and np.array_equal(host(q), ref_q)
+
+
+def test_swiglu_of_what_is_no_number(qg):
+    """The formula's values: silu(inf) = inf, silu(-inf) = -inf / inf = NaN."""
+    note("swiglu inf, nan")
+    g = np.array([np.inf, -np.inf, np.nan, np.inf, 0.0, 2.0, -2.0, 0.0], np.float32)
+    u = np.array([1.0, 1.0, 1.0, -2.0, np.inf, np.inf, np.inf, np.nan], np.float32)
+    y = host(qg.swiglu(dev(np.concatenate([g, u])[None]), out_dtype=torch.float32))[0]
+    assert np.array_equal(y, np.array([np.inf, np.nan, np.nan, -np.inf, np.nan, np.inf, -np.inf, np.nan], np.float32), equal_nan=True)
