@@ -176,13 +176,14 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void fp8_row_kernel(RowParams p)
                 }
                 return lanes_sum<L>(t, red);
             };
-            const float ss = sum_sq(1.0f);
-            float f = 1.0f / __builtin_sqrtf(ss * p.inv_k + p.eps);
-            // Squares above fp32's range (|h| from 1.8e19 on): again with h 2^-80,
-            // beside which eps is nothing.  Rows of 16 lanes share the branch.
-            if (__any(!(ss <= 3.40282347e38f))) {
-                const float small = sum_sq(8.27180613e-25f);  // 2^-80
-                if (!(ss <= 3.40282347e38f)) f = 8.27180613e-25f / __builtin_sqrtf(small * p.inv_k);
+            const float mean = sum_sq(1.0f) * p.inv_k + p.eps;
+            float f = 1.0f / __builtin_sqrtf(mean);
+            // Squares above fp32's range (|h| from 1.8e19 on), or their mean with eps: again
+            // with h 2^-80 and eps 2^-160.  Rows of 16 lanes share the branch.
+            if (__any(!(mean <= 3.40282347e38f))) {
+                constexpr float kSmall = 8.27180613e-25f;  // 2^-80
+                const float small = sum_sq(kSmall) * p.inv_k + p.eps * kSmall * kSmall;
+                if (!(mean <= 3.40282347e38f)) f = kSmall / __builtin_sqrtf(small);
             }
 #pragma unroll
             for (int j = 0; j < NP; ++j) {

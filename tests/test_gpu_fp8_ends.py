@@ -144,3 +144,30 @@ def test_swiglu_of_what_is_no_number(qg):
     u = np.array([1.0, 1.0, 1.0, -2.0, np.inf, np.inf, np.inf, np.nan], np.float32)
     y = host(qg.swiglu(dev(np.concatenate([g, u])[None]), out_dtype=torch.float32))[0]
     assert np.array_equal(y, np.array([np.inf, np.nan, np.nan, -np.inf, np.nan, np.inf, -np.inf, np.nan], np.float32), equal_nan=True)
+
+
+@pytest.mark.parametrize("k", [8, 128, 384, 4096, 32768])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_rms_norm_with_a_large_eps(qg, k, bf16):
+    """eps up to fp32's largest value beside rows whose squares leave the range,
+    and beside rows whose squares do not but whose sum with eps does.  26 half
+    steps as for every norm; scaling by powers of two adds none.  Results below
+    2^-126 keep steps of 2^-149."""
+    note("norm eps k=%d bf16=%s" % (k, bf16))
+    g = synth.rng(k)
+    scale = np.array([1.0, 1e15, 1e18, 4e18, 1.8e19, 3e19, 2e20, 1e22, 1e30, 0.0])[:, None]
+    x = (g.uniform(0.5, 1.0, (10, k)) * np.where(g.random((10, k)) < 0.5, -1, 1) * scale).astype(np.float32)
+    r = (g.uniform(-0.2, 0.2, (10, k)) * scale).astype(np.float32)
+    w = (1 + g.random(k)).astype(np.float32)
+    if bf16:
+        xb, rb = synth.to_bf16_bits(x), synth.to_bf16_bits(r)
+        x, r = synth.bf16_bits_to_f32(xb), synth.bf16_bits_to_f32(rb)
+        xd, rd = dev_bf16(xb), dev_bf16(rb)
+    else:
+        xd, rd = dev(x), dev(r)
+    for eps in (1e-6, 1.0, 1e30, 1e36, 1e38, 3.3e38, float(np.finfo(np.float32).max)):
+        for res in (None, r):
+            v, _ = fp8.rms_norm(x, w, float(np.float32(eps)), res)
+            y = host(qg.rms_norm(xd, dev(w), eps, None if res is None else rd, None if res is None else torch.empty_like(rd),
+                                 out_dtype=torch.float32))
+            assert np.all(np.abs(y - v) <= 26 * HALF * np.abs(v) + 2.0 ** -149), (eps, res is None)
