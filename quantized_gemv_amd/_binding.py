@@ -393,7 +393,7 @@ def pack_tiles16(codes: torch.Tensor, out: torch.Tensor = None):
     out = torch.empty(nb, dtype=torch.int8, device=codes.device) if out is None else out
     if out.numel() < nb:
         raise ValueError("out holds %d bytes, %d needed" % (out.numel(), nb))
-    _check(lib().qg_pack_tiles16(_p(codes), n, k, _p(out), _stream(codes)), "qg_pack_tiles16")
+    _call("qg_pack_tiles16", codes, codes.data_ptr(), n, k, out.data_ptr())
     return out
 
 

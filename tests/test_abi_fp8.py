@@ -269,3 +269,15 @@ def test_launches_keep_their_memory(qg, monkeypatch):
     at = w.data_ptr()
     w.data = torch.zeros(256)
     assert at in [s.data_ptr() for s in a._keep]
+
+
+def test_tiles_are_made_on_the_codes_device(qg, monkeypatch):
+    """As the other calls of the path: the matrix's device need not be the current one."""
+    from quantized_gemv_amd import _binding as b
+    monkeypatch.setattr(b, "_dev", lambda t, *a: t)
+    sent = []
+    monkeypatch.setattr(b, "_call", lambda name, x, *a: sent.append((name, x.data_ptr())))
+    W = qg.QWeight(qg.QG_WFMT_FP8, 130, 256, torch.zeros(130, 256).to(torch.float8_e4m3fn), torch.zeros(2, 2))
+    T = qg.tiled16(W)
+    assert sent == [("qg_pack_tiles16", W.codes.data_ptr())]
+    assert T.fmt == qg.QG_WFMT_FP8_T16 and T.codes.numel() == 144 * 256
