@@ -136,7 +136,8 @@ __device__ __forceinline__ Out output_of(const Fp8Params& p) { return {p.y, p.yt
 // requested in whole lines, eight lanes to the 128 bytes of each, and pass
 // through the wave's own LDS into the order of the matrix instruction (requested
 // in that order, 16 bytes here and there: 16 x 22016 x 4096 row-major 22.5 against
-// 19.0 us, 64 x 11008 x 4096 in tiles 21.5 against 17.4); the next block is
+// 19.0 us, 64 x 11008 x 4096 in tiles, where bf16 outputs now come from 64 x 64 tiles,
+// 21.5 against 17.4); the next block is
 // requested as soon as they are there.  Blocks past the last are requested past
 // the end of the buffer, which reads zeros and moves nothing; their step is 0, as
 // the last block's, which is read again for them, may be infinite.  ONCE: the
