@@ -171,3 +171,16 @@ def test_rms_norm_with_a_large_eps(qg, k, bf16):
             y = host(qg.rms_norm(xd, dev(w), eps, None if res is None else rd, None if res is None else torch.empty_like(rd),
                                  out_dtype=torch.float32))
             assert np.all(np.abs(y - v) <= 26 * HALF * np.abs(v) + 2.0 ** -149), (eps, res is None)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 200, 384), (30, 4200, 384), (600, 1300, 1152), (298, 1024, 9984)])
+def test_steps_whose_product_is_below_the_normal_numbers(qg, m, n, k):
+    """s_x s_w of 2^-148: kept as fp32 keeps it, so whole sums come out exactly."""
+    note("small steps m=%d n=%d k=%d" % (m, n, k))
+    g = synth.rng(m + k)
+    x, w = positive(g, m, k), positive(g, n, k)
+    s_x, s_w = np.full((k // 128, m), 2.0 ** -126, np.float32), np.full((-(-n // 128), k // 128), 2.0 ** -22, np.float32)
+    ref = (fp8.decode(x) @ fp8.decode(w).T) * 2.0 ** -148  # sums up to 64 k, below 2^24
+    W = qg.QWeight(qg.QG_WFMT_FP8, n, k, dev(w).view(E4), dev(s_w))
+    y = host(qg.qgemm_fp8(W, dev(x).view(E4), dev(s_x), y_dtype=torch.float32))
+    assert np.array_equal(y.astype(np.float64), ref)
